@@ -57,6 +57,9 @@ extern "C" {
  * pages): every token and page index of a head then fits 32-bit arithmetic with room to spare. */
 #define TG_MAX_HEAD_TOKENS (1 << 30)
 
+/* Most drafted tokens of one sequence in a tree step (a token's mask is 64 bits). */
+#define TG_MAX_DRAFT 64
+
 typedef struct CUstream_st *tg_stream; /* == cudaStream_t */
 
 /* Shape of one decode step over one layer. */
@@ -136,6 +139,22 @@ int tg_share_segment(tg_alloc *a, int32_t n_tokens, int32_t n_heads, int32_t *se
 int tg_reserve(tg_alloc *a, int32_t seq_id, int32_t n_heads, const int32_t *kv_len,
                int32_t n_prefix, const int32_t *prefix_segs, int32_t *page_ids,
                int64_t capacity, int32_t *head_count, int64_t *n_written);
+/* Fork ("RadixAttention and KV reuse": requests share the pages of their common prefix and depart
+ * from it): a new sequence child with the parent's tokens. Per KV head h (n_heads as reserved): the
+ * parent holds held[h] tokens; the child reserves kv_len[h] >= held[h] tokens (its budget) and
+ * references the parent's first shared_pages[h] pages, which must be full
+ * (shared_pages[h] * page <= held[h]) and must not be written by either sequence from then on (under
+ * the sink + recent rule: pages of sinks, or of a prefix shared already). The rest of its pages are
+ * private pages from the free list. page_ids / capacity / head_count / n_written as tg_reserve.
+ * Pages of the parent that hold further tokens are to be copied into the child's: copy_src,
+ * copy_dst and copy_rows (host, copy_capacity entries) receive those *n_copies pairs with their
+ * used rows, as tg_copy_pages takes them. A forked sequence is released and forked like any other.
+ * All-or-nothing: TG_ENOSPC leaves state unchanged; TG_ENOTFOUND for an unknown parent, TG_EEXIST
+ * for a known child, TG_EINVAL for lengths that do not fit or too small a buffer. */
+int tg_fork(tg_alloc *a, int32_t parent, int32_t child, int32_t n_heads, const int32_t *held,
+            const int32_t *kv_len, const int32_t *shared_pages, int32_t *page_ids,
+            int64_t capacity, int32_t *head_count, int32_t *copy_src, int32_t *copy_dst,
+            int32_t *copy_rows, int64_t copy_capacity, int64_t *n_copies, int64_t *n_written);
 /* Release a sequence: private pages return to the free list, shared pages drop one reference. */
 int tg_release(tg_alloc *a, int32_t seq_id);
 /* Drop a segment's own reference; its pages return once no sequence reads them. */
@@ -634,6 +653,159 @@ int tg_tiered_append_int4(const tg_shape *shape, const void *k_new, const void *
                           const int32_t *head_slow_cap, int32_t *head_kv_len,
                           int32_t *head_fast_len, int32_t *moved_out, int32_t *slot_out,
                           tg_stream stream);
+
+/* =====================================================================================
+ * Speculative step (no counterpart on the pages: drafted tokens verified against the same ragged
+ * cache that the decode step reads; tree verification: Miao et al. 2023, SpecInfer; Cai et al.
+ * 2024, Medusa). One step: tg_qk_norm_rope on the drafted tokens' projections, tg_tree_decode, and
+ * after the caller's choice of an accepted path tg_append_path_sink_recent. The drafted tokens of a
+ * batch are laid end to end: sequence b has tokens draft_off[b] .. draft_off[b+1]-1 (device int32
+ * [B+1], ascending), at most TG_MAX_DRAFT, possibly none. Token-major arrays [n][heads][D] are
+ * given with the distance between tokens in elements (their stride, a multiple of 8 and at least
+ * heads*D), so that q, k and v may be slices of one fused projection.
+ * ===================================================================================== */
+
+/* Frequencies of rotary positions (Su et al. 2021) for rot_dim (even) rotated elements: inv_freq
+ * (host fp64 [rot_dim/2]) and rot_scale, a factor of the rotation (1 except under YARN).
+ *   NONE:   inv_freq[i] = base^(-2i/rot_dim)                       (base > 1)
+ *   LINEAR: positions interpolated (Chen et al. 2023): inv_freq / factor
+ *   NTK:    base * factor^(rot_dim/(rot_dim-2)) in place of base   (rot_dim != 2)
+ *   YARN:   Peng et al. 2023: pairs that turn more than beta_fast times over orig_len positions
+ *           keep their frequency, those below beta_slow turns get inv_freq / factor, linear in the
+ *           pair index between; rot_scale = 0.1 ln(factor) + 1
+ * factor >= 1; orig_len, beta_fast, beta_slow are YARN's only. TG_EINVAL otherwise. */
+#define TG_ROPE_NONE 0
+#define TG_ROPE_LINEAR 1
+#define TG_ROPE_NTK 2
+#define TG_ROPE_YARN 3
+int tg_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double factor,
+                        int64_t orig_len, double beta_fast, double beta_slow, double *inv_freq,
+                        float *rot_scale);
+
+/* Norm of every query and key head and rotary position in one pass. Per token n and head:
+ *   y = x * (mean_d x_d^2 + eps)^(-1/2) * w      (w = q_weight / k_weight, bf16 [D]; NULL: y = x)
+ *   (a, b) -> rot_scale * (a cos t - b sin t, a sin t + b cos t), t = position[n] * inv_freq[i],
+ * over the pairs i < rot_dim/2 of y's first rot_dim elements: (y[2i], y[2i+1]) with interleaved
+ * != 0, else (y[i], y[i + rot_dim/2]); the rest of y is kept. fp32 throughout, t in fp64, one
+ * rounding to bf16. q bf16 [n_tokens][Hq][D], k bf16 [n_tokens][Hkv][D] with token strides; Hq or
+ * Hkv may be 0 (that side is skipped, its pointers unused). position int32 [n_tokens], any value;
+ * inv_freq device fp64 [rot_dim/2] (both may be NULL when rot_dim = 0). An output may be its own
+ * input (same pointer and stride). TG_EUNSUPPORTED: D % 8 != 0, D > 256, or halves with
+ * rot_dim % 16 != 0. One launch; moves 4*D bytes per head. */
+int tg_qk_norm_rope(int64_t n_tokens, int32_t Hq, int32_t Hkv, int32_t D, const void *q,
+                    int64_t q_stride, const void *k, int64_t k_stride, const void *q_weight,
+                    const void *k_weight, float eps, const int32_t *position,
+                    const double *inv_freq, int32_t rot_dim, int32_t interleaved,
+                    float rot_scale, void *q_out, int64_t q_out_stride, void *k_out,
+                    int64_t k_out_stride, tg_stream stream);
+
+/* Masks of a draft tree: parent[draft_off[b] + j] is the index within sequence b of token j's
+ * parent, -1 for a token that follows the cache directly; parents come before their children
+ * (TG_EINVAL otherwise). mask[n] gets bit i for every ancestor i of the token and for itself.
+ * All arrays host; draft_off[0] = 0. */
+int tg_tree_masks(int32_t B, const int32_t *draft_off, const int32_t *parent, uint64_t *mask);
+
+/* Plan of tree attention steps: the heads' reserved pages laid end to end and cut into equal
+ * shares, one per resident CTA, ahead of time. kv_cap[B*Hkv] (host): reserved tokens of each head
+ * (its budget); every call reads the current lengths from the device, which must fit them, so a
+ * growing head needs no new plan (as tg_plan_opts.capacity). max_draft: most drafted tokens of a
+ * sequence (1 .. TG_MAX_DRAFT). group_of_head, group_off, n_groups (host) bound the page-table rows
+ * as in tg_plan_create. num_workers 0 = one resident wave. host_only 1: work list only (inspection).
+ * device -1 = current. wait_limit_us bounds any single wait in the kernel (0 = 4 s).
+ * Owns one device allocation (work list, partial results of split heads, error word), made here;
+ * calls on one plan share it, so they must be ordered (one stream, or events between).
+ * Serves page = 16, D 64 or 128, G 1, 2, 4 or 8, pools below 2^27 pages (TG_EUNSUPPORTED otherwise).
+ * TG_EINVAL for other bad arguments; TG_ENOMEM; *out is NULL on error. */
+typedef struct tg_tree_plan tg_tree_plan;
+int tg_tree_plan_create(const tg_shape *shape, const int32_t *kv_cap, int32_t max_draft,
+                        const int32_t *group_of_head, const int64_t *group_off, int32_t n_groups,
+                        int32_t num_workers, int32_t host_only, int32_t device,
+                        int32_t wait_limit_us, tg_tree_plan **out);
+void tg_tree_plan_destroy(tg_tree_plan *p);
+/* Inspection: counts, and for non-NULL arrays the work items (n_items x 8 int32: b*Hkv + h,
+ * page_begin, page_end, partial slot (-1 = writes the final output), first query row, 1 if the item
+ * takes the drafted tokens, reserved tokens, 0) and each worker's first item [n_workers + 1]. */
+int tg_tree_plan_items(const tg_tree_plan *p, int32_t *n_items, int32_t *n_workers,
+                       int32_t *n_merge, int64_t *device_bytes, int32_t *items,
+                       int32_t *worker_off);
+/* As tg_plan_status, for the calls on a tree plan. */
+int tg_tree_plan_status(tg_tree_plan *p, tg_stream stream);
+
+/* Attention of the drafted tokens over the ragged paged cache and over each other. For drafted
+ * token t (index i within sequence b) and query head hq, h = hq / G, over the n = head_kv_len[b*Hkv+h]
+ * retained tokens (read through the page table as in tg_ragged_paged_decode) and the drafted
+ * tokens j of the sequence with bit j of tree_mask[t] set (bits past the sequence's draft are
+ * ignored; the token itself counts only if its bit is set):
+ *   s = scale * q . k;  softcap > 0: s <- softcap * tanh(s / softcap);
+ *   lse = ln sum exp(s), out = sum exp(s - lse) v;  nothing to attend to: out = 0, lse = -inf.
+ * What other places hold (rows of a page past the head's tokens, drafted tokens outside the mask)
+ * does not reach the result, infinities and NaN included.
+ *   q bf16 [n_tokens][Hq][D], k_draft / v_draft bf16 [n_tokens][Hkv][D] (device, token strides);
+ *   tree_mask device uint64 [n_tokens]; k_pages .. head_kv_len as tg_ragged_paged_decode;
+ *   out bf16 [n_tokens][Hq][D] and lse fp32 [n_tokens][Hq], contiguous; rows behind the last
+ *   sequence are left as they were. n_tokens: rows of these arrays, >= draft_off[B].
+ * A drafted token alone (mask bit 0) is a decode step whose token is not in the cache yet.
+ * bf16 products, fp32 accumulation, P rounded to bf16; deterministic. One kernel, and a merge
+ * kernel (programmatic dependent) when the plan splits heads. Sequences whose draft does not fit
+ * the plan or n_tokens, and lengths above the reserved ones, are skipped (TG_EBADPAGE through
+ * tg_tree_plan_status; their rows are unspecified), as are bad page ids and rows. */
+int tg_tree_decode(tg_tree_plan *plan, int64_t n_tokens, const int32_t *draft_off, const void *q,
+                   int64_t q_stride, const void *k_draft, int64_t k_stride, const void *v_draft,
+                   int64_t v_stride, const uint64_t *tree_mask, const void *k_pages,
+                   const void *v_pages, const int32_t *page_table, const int64_t *head_page_off,
+                   const int32_t *head_kv_len, float scale, float softcap, void *out, float *lse,
+                   tg_stream stream);
+
+/* Append of an accepted path under the sink + recent rule: path[b][0 .. path_len[b]-1] (int32
+ * [B][max_path], device) are indices within sequence b's draft, appended in order with the result
+ * of as many tg_append_sink_recent calls. max_path 1 .. 64 (TG_EUNSUPPORTED above).
+ * head_kv_len and head_cursor are read; kv_len_out and cursor_out (int32 [B*Hkv]) receive the new
+ * ones and may be the same arrays. slot_out (int32 [B*Hkv][max_path]): where each token of the path
+ * is kept, -1 past the path and for tokens that a later one of the same path replaced. A head with
+ * budget < 1, or whose path_len, draft range, path index or page id is out of bounds, is left as it
+ * was (all slots -1). k_draft / v_draft bf16 [n_draft][Hkv][D] with token strides. One launch. */
+int tg_append_path_sink_recent(const tg_shape *shape, int32_t sink, int64_t n_draft,
+                               const int32_t *draft_off, int32_t max_path, const int32_t *path,
+                               const int32_t *path_len, const void *k_draft, int64_t k_stride,
+                               const void *v_draft, int64_t v_stride, void *k_pages,
+                               void *v_pages, const int32_t *page_table,
+                               const int64_t *head_page_off, const int32_t *head_budget,
+                               const int32_t *head_kv_len, const int32_t *head_cursor,
+                               int32_t *kv_len_out, int32_t *cursor_out, int32_t *slot_out,
+                               tg_stream stream);
+
+/* =====================================================================================
+ * Moving tokens between pages.
+ * ===================================================================================== */
+
+/* Copy pages within a pool pair: for i < n_copies the first rows[i] rows (0 .. 16; rows NULL: all)
+ * of page src_page[i] to page dst_page[i], K and V (and, when given, the scales of a quantised
+ * tier, fp32 [num_pages][16]). Pools [num_pages][16][row_bytes], row_bytes a multiple of 16 up to
+ * 4096 (TG_EUNSUPPORTED): 2*D for bf16, D for INT8, D/2 for INT4. A page may be the source of many
+ * copies; a destination must be no other copy's destination or source (src = dst: nothing to do).
+ * Pairs with a page outside the pool or rows outside 0 .. 16 are skipped and counted: n_bad (device
+ * int32 [1]) grows by one each; the caller clears it. Index arrays device int32. One launch. */
+int tg_copy_pages(int64_t num_pages, int32_t row_bytes, int64_t n_copies, const int32_t *src_page,
+                  const int32_t *dst_page, const int32_t *rows, void *k_pool, void *v_pool,
+                  float *k_scale, float *v_scale, int32_t *n_bad, tg_stream stream);
+
+/* Compaction of a prompt's rows to the heads' budgets ("Tangram" 三大机制 1: after compression a
+ * head holds only its budget). Head i = b*Hkv + h keeps source tokens keep_idx[keep_off[i]] ..
+ * keep_idx[keep_off[i+1]-1] (device int32 [n_keep] and int64 [B*Hkv+1], any order, repeats
+ * allowed); the j-th becomes token j of the head's row of page_table (page and slot as in the
+ * decode calls). Source rows: token t in page src_table[src_head_off[i] + t/16] of k_src / v_src
+ * (bf16 [src_num_pages][16][D]), src_len[i] tokens. The source pools may be the destination pools
+ * when no written page is also read. head_kv_len[i] receives the count. shape: B, Hkv, D
+ * (D % 8 == 0), page 16, num_pages of the destination. n_bad (device int32 [1], cleared by the
+ * caller) grows by one per head whose list is unusable (offsets out of order or past n_keep, or
+ * more than head_budget[i] tokens: nothing is written, length 0) and per row with a token or page
+ * out of bounds (not written). One launch. */
+int tg_compact_kv(const tg_shape *shape, int64_t src_num_pages, const void *k_src,
+                  const void *v_src, const int32_t *src_table, const int64_t *src_head_off,
+                  const int32_t *src_len, const int64_t *keep_off, const int32_t *keep_idx,
+                  int64_t n_keep, void *k_pages, void *v_pages, const int32_t *page_table,
+                  const int64_t *head_page_off, const int32_t *head_budget, int32_t *head_kv_len,
+                  int32_t *n_bad, tg_stream stream);
 
 /* =====================================================================================
  * SplitZip: lossless BF16 codec for KV transfer ("SplitZip" explainer, arXiv 2605.01708, "Die

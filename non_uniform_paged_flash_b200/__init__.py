@@ -22,6 +22,8 @@ LIB_PATH = os.path.join(_PKG, "libtg.so")
 
 TG_OK, TG_EINVAL, TG_ENOSPC, TG_EBADPAGE, TG_ECUDA, TG_ETIMEOUT = 0, 1, 2, 3, 4, 5
 TG_ENOMEM, TG_ENOTFOUND, TG_EUNSUPPORTED, TG_EEXIST = 6, 7, 8, 9
+TG_MAX_DRAFT = 64              # most drafted tokens of one sequence in a tree step
+TG_ROPE_NONE, TG_ROPE_LINEAR, TG_ROPE_NTK, TG_ROPE_YARN = 0, 1, 2, 3
 TG_MAX_HEAD_TOKENS = 1 << 30   # longest retained length of one (sequence, KV head) a plan accepts
 
 
@@ -69,6 +71,7 @@ CASCADE_ROWS = 256
 
 # (name, restype, argtypes)
 _P, _I32, _I64, _F32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+_F64 = ctypes.c_double
 _SIGS = [
     ("tg_strerror", ctypes.c_char_p, [ctypes.c_int]),
     ("tg_last_cuda_error", ctypes.c_char_p, []),
@@ -81,6 +84,8 @@ _SIGS = [
     ("tg_alloc_refcount", _I32, [_P, _I32]),
     ("tg_share_segment", ctypes.c_int, [_P, _I32, _I32, _P, _P]),
     ("tg_reserve", ctypes.c_int, [_P, _I32, _I32, _P, _I32, _P, _P, _I64, _P, _P]),
+    ("tg_fork", ctypes.c_int, [_P, _I32, _I32, _I32, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _I64, _P,
+                               _P]),
     ("tg_release", ctypes.c_int, [_P, _I32]),
     ("tg_release_segment", ctypes.c_int, [_P, _I32]),
     ("tg_build_group_tables", ctypes.c_int, [_I32, _I32, _P, _P, _I32, _P, _P, _P, _P]),
@@ -120,6 +125,24 @@ _SIGS = [
                                         _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     ("tg_tiered_append_int4", ctypes.c_int, [ctypes.POINTER(tg_shape), _P, _P, _P, _P, _P, _P, _P,
                                              _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    ("tg_rope_frequencies", ctypes.c_int, [_I32, _F64, _I32, _F64, _I64, _F64, _F64, _P,
+                                           ctypes.POINTER(_F32)]),
+    ("tg_qk_norm_rope", ctypes.c_int, [_I64, _I32, _I32, _I32, _P, _I64, _P, _I64, _P, _P, _F32, _P,
+                                       _P, _I32, _I32, _F32, _P, _I64, _P, _I64, _P]),
+    ("tg_tree_masks", ctypes.c_int, [_I32, _P, _P, _P]),
+    ("tg_tree_plan_create", ctypes.c_int, [ctypes.POINTER(tg_shape), _P, _I32, _P, _P, _I32, _I32,
+                                           _I32, _I32, _I32, ctypes.POINTER(_P)]),
+    ("tg_tree_plan_destroy", None, [_P]),
+    ("tg_tree_plan_items", ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P]),
+    ("tg_tree_plan_status", ctypes.c_int, [_P, _P]),
+    ("tg_tree_decode", ctypes.c_int, [_P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P,
+                                      _P, _F32, _F32, _P, _P, _P]),
+    ("tg_append_path_sink_recent", ctypes.c_int, [ctypes.POINTER(tg_shape), _I32, _I64, _P, _I32, _P,
+                                                  _P, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _P, _P,
+                                                  _P, _P, _P, _P]),
+    ("tg_copy_pages", ctypes.c_int, [_I64, _I32, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    ("tg_compact_kv", ctypes.c_int, [ctypes.POINTER(tg_shape), _I64, _P, _P, _P, _P, _P, _P, _P, _I64,
+                                     _P, _P, _P, _P, _P, _P, _P, _P]),
     ("tg_splitzip_workspace_bytes", _I64, [_I64]),
     ("tg_splitzip_encode", ctypes.c_int, [_I64, _P, _P, _P, _P, _P, _P, _I64, _P, _P, _P]),
     ("tg_splitzip_decode", ctypes.c_int, [_I64, _P, _P, _P, _P, _P, _P, _I64, _P, _P]),
@@ -318,6 +341,24 @@ def tg_reserve(a, seq_id: int, kv_len, prefix_segs=(), page: int = None,
                              ctypes.byref(n)), "tg_reserve")
     ids = ids[:n.value].copy()
     return (ids, counts) if with_counts else ids
+
+
+def tg_fork(a, parent: int, child: int, held, kv_len, shared_pages):
+    """Fork a sequence: returns (page_ids flat, head_count, copy_src, copy_dst, copy_rows); the
+    last three are the pages to hand to tg_copy_pages."""
+    held, kv, sh = (_h(x, np.int32).reshape(-1) for x in (held, kv_len, shared_pages))
+    _count(held, kv.size, "held")
+    _count(sh, kv.size, "shared_pages")
+    page = _alloc_page(a, None) or 1
+    cap = int((np.maximum(kv, 0).astype(np.int64) // page + 1).sum())
+    ids = np.empty(cap, dtype=np.int32)
+    counts = np.empty(kv.size, dtype=np.int32)
+    src, dst, rows = (np.empty(cap, dtype=np.int32) for _ in range(3))
+    n, m = ctypes.c_int64(), ctypes.c_int64()
+    _check(_lib().tg_fork(a, parent, child, kv.size, _hp(held), _hp(kv), _hp(sh), _hp(ids), cap,
+                          _hp(counts), _hp(src), _hp(dst), _hp(rows), cap, ctypes.byref(m),
+                          ctypes.byref(n)), "tg_fork")
+    return ids[:n.value].copy(), counts, src[:m.value].copy(), dst[:m.value].copy(), rows[:m.value].copy()
 
 
 def tg_release(a, seq_id: int):
@@ -802,6 +843,277 @@ def tg_quantize_int4(src, packed, scale, stream=None):
         _bytes(scale, 4 * n_rows, "scale")
     _check(_lib().tg_quantize_int4(n_rows, D, _dp(src), _dp(packed), _dp(scale), _stream(stream)),
            "tg_quantize_int4")
+
+
+# ---------------------------------------------------------------------------------------
+# Speculative step and page moves (see include/tg.h).
+# ---------------------------------------------------------------------------------------
+
+def _same_device(**tensors):
+    """Every tensor is on the current CUDA device (the calls launch there)."""
+    import torch
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not getattr(t, "is_cuda", False):
+            raise ValueError(f"{name}: expected a CUDA tensor")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _tokens(t, what, heads=None, D=None, n=None):
+    """A bf16 [n, heads, D] tensor whose tokens' rows are contiguous: its token stride."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{what}: expected bf16 [tokens, heads, D]")
+    if (heads is not None and t.shape[1] != heads) or (D is not None and t.shape[2] != D) or \
+            (n is not None and t.shape[0] != n):
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected [{n}, {heads}, {D}]")
+    if t.numel() and ((t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise ValueError(f"{what}: each token's heads must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def tg_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = TG_ROPE_NONE,
+                        factor: float = 1.0, orig_len: int = 0, beta_fast: float = 32.0,
+                        beta_slow: float = 1.0):
+    """(inv_freq float64[rot_dim // 2], rot_scale) for tg_qk_norm_rope (upload inv_freq)."""
+    inv = np.empty(max(0, int(rot_dim) // 2), dtype=np.float64)
+    scale = ctypes.c_float()
+    _check(_lib().tg_rope_frequencies(int(rot_dim), float(base), int(scaling), float(factor),
+                                      int(orig_len), float(beta_fast), float(beta_slow), _hp(inv),
+                                      ctypes.byref(scale)), "tg_rope_frequencies")
+    return inv, scale.value
+
+
+def tg_qk_norm_rope(q, k, q_weight, k_weight, eps: float, position, inv_freq, q_out, k_out,
+                    interleaved: bool = False, rot_scale: float = 1.0, stream=None):
+    """Head norms and rotary positions of q [n, Hq, D] and k [n, Hkv, D] (either may be None);
+    rot_dim = 2 * inv_freq.numel()."""
+    import torch
+    side = q if q is not None else k
+    if side is None:
+        raise ValueError("q and k: one must be given")
+    _same_device(q=q, k=k, q_weight=q_weight, k_weight=k_weight, position=position, inv_freq=inv_freq,
+                 q_out=q_out, k_out=k_out)
+    n, _, D = side.shape if side.dim() == 3 else (0, 0, 0)
+    args = []
+    for name, x, y, w in (("q", q, q_out, q_weight), ("k", k, k_out, k_weight)):
+        if x is None:
+            args.append((0, None, 0, None, None, 0))
+            continue
+        if y is None:
+            raise ValueError(f"{name}_out: missing")
+        st = _tokens(x, name, None, D, n)
+        so = _tokens(y, name + "_out", x.shape[1], D, n)
+        if w is not None:
+            _need(w, D, torch.bfloat16, name + "_weight")
+        args.append((x.shape[1], _dp(x), st, _dp(w), _dp(y), so))
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if rot and n:
+        _need(inv_freq, rot // 2, torch.float64, "inv_freq")
+        _need(position, n, torch.int32, "position")
+    (Hq, qp, qs, qw, qo, qos), (Hk, kp, ks, kw, ko, kos) = args
+    _check(_lib().tg_qk_norm_rope(n, Hq, Hk, D, qp, qs, kp, ks, qw, kw, float(eps), _dp(position),
+                                  _dp(inv_freq), rot, int(bool(interleaved)), float(rot_scale), qo,
+                                  qos, ko, kos, _stream(stream)), "tg_qk_norm_rope")
+
+
+def tg_tree_masks(draft_off, parent) -> np.ndarray:
+    """uint64 mask of every drafted token (view as int64 to upload) from its parent's index."""
+    off = _h(draft_off, np.int32).reshape(-1)
+    par = _h(parent, np.int32).reshape(-1)
+    _count(off, 1, "draft_off", at_least=True)
+    _count(par, int(off[-1]), "parent")
+    mask = np.zeros(par.size, dtype=np.uint64)
+    _check(_lib().tg_tree_masks(off.size - 1, _hp(off), _hp(par), _hp(mask)), "tg_tree_masks")
+    return mask
+
+
+@dataclass
+class TreePlan:
+    """Owns a tg_tree_plan handle; destroy() (or garbage collection) frees it."""
+    handle: ctypes.c_void_p
+    shape: tg_shape
+    max_draft: int
+
+    def destroy(self):
+        if self.handle:
+            _lib().tg_tree_plan_destroy(self.handle)
+            self.handle = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:
+            pass
+
+
+def tg_tree_plan_create(shape: tg_shape, kv_cap, max_draft: int, group_of_head, group_off,
+                        num_workers: int = 0, host_only: bool = False, device: int = -1,
+                        wait_limit_us: int = 0) -> TreePlan:
+    cap = _h(kv_cap, np.int32).reshape(-1)
+    goh = _h(group_of_head, np.int32).reshape(-1)
+    goff = _h(group_off, np.int64).reshape(-1)
+    _count(cap, shape.B * shape.Hkv, "kv_cap")
+    _count(goh, shape.Hkv, "group_of_head")
+    _count(goff, 2, "group_off", at_least=True)
+    h = ctypes.c_void_p()
+    _check(_lib().tg_tree_plan_create(ctypes.byref(shape), _hp(cap), int(max_draft), _hp(goh),
+                                      _hp(goff), goff.size - 1, int(num_workers), int(host_only),
+                                      int(device), int(wait_limit_us), ctypes.byref(h)),
+           "tg_tree_plan_create")
+    return TreePlan(h, shape, int(max_draft))
+
+
+def tg_tree_plan_destroy(plan: TreePlan):
+    plan.destroy()
+
+
+def tg_tree_plan_items(plan: TreePlan) -> dict:
+    """Counts, items int32[n, 8] and worker_off int32[n_workers + 1] (see include/tg.h)."""
+    n, w, m, nbytes = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int64()
+    refs = [ctypes.byref(x) for x in (n, w, m, nbytes)]
+    _check(_lib().tg_tree_plan_items(plan.handle, *refs, None, None), "tg_tree_plan_items")
+    items = np.empty((n.value, 8), dtype=np.int32)
+    off = np.empty(w.value + 1, dtype=np.int32)
+    _check(_lib().tg_tree_plan_items(plan.handle, *refs, _hp(items), _hp(off)), "tg_tree_plan_items")
+    return dict(n_items=n.value, n_workers=w.value, n_merge=m.value, device_bytes=nbytes.value,
+                items=items, worker_off=off)
+
+
+def tg_tree_plan_status(plan: TreePlan, stream=None) -> int:
+    return int(_lib().tg_tree_plan_status(plan.handle, _stream(stream)))
+
+
+def _pool(t, pages, D, what):
+    import torch
+    if pages > 0:
+        _need(t, pages * 16 * D, torch.bfloat16, what)
+
+
+def tg_tree_decode(plan: TreePlan, draft_off, q, k_draft, v_draft, tree_mask, k_pages, v_pages,
+                   page_table, head_page_off, head_kv_len, scale: float, softcap: float, out, lse,
+                   stream=None):
+    """Tree attention of drafted tokens (q [n, Hq, D], k_draft / v_draft [n, Hkv, D]) over the cache
+    and each other; tree_mask int64 / uint64 [n]."""
+    import torch
+    s = plan.shape
+    _same_device(draft_off=draft_off, q=q, k_draft=k_draft, v_draft=v_draft, tree_mask=tree_mask,
+                 k_pages=k_pages, v_pages=v_pages, page_table=page_table, head_page_off=head_page_off,
+                 head_kv_len=head_kv_len, out=out, lse=lse)
+    n = q.shape[0]
+    qs = _tokens(q, "q", s.Hq, s.D)
+    ks = _tokens(k_draft, "k_draft", s.Hkv, s.D, n)
+    vs = _tokens(v_draft, "v_draft", s.Hkv, s.D, n)
+    if tree_mask.dtype not in (torch.int64, torch.uint64):
+        raise ValueError(f"tree_mask: expected 64-bit integers, got {tree_mask.dtype}")
+    _need(tree_mask, n, tree_mask.dtype, "tree_mask")
+    _need(draft_off, s.B + 1, torch.int32, "draft_off")
+    _need(head_page_off, s.B * s.Hkv, torch.int64, "head_page_off")
+    _need(head_kv_len, s.B * s.Hkv, torch.int32, "head_kv_len")
+    _need(page_table, 0, torch.int32, "page_table")
+    _pool(k_pages, s.num_pages, s.D, "k_pages")
+    _pool(v_pages, s.num_pages, s.D, "v_pages")
+    _need(out, n * s.Hq * s.D, torch.bfloat16, "out")
+    _need(lse, n * s.Hq, torch.float32, "lse")
+    _check(_lib().tg_tree_decode(
+        plan.handle, n, _dp(draft_off), _dp(q), qs, _dp(k_draft), ks, _dp(v_draft), vs,
+        _dp(tree_mask), _dp(k_pages), _dp(v_pages), _dp(page_table), _dp(head_page_off),
+        _dp(head_kv_len), float(scale), float(softcap), _dp(out), _dp(lse), _stream(stream)),
+        "tg_tree_decode")
+
+
+def tg_append_path_sink_recent(shape: tg_shape, sink: int, draft_off, path, path_len, k_draft, v_draft,
+                               k_pages, v_pages, page_table, head_page_off, head_budget, head_kv_len,
+                               head_cursor, kv_len_out, cursor_out, slot_out, stream=None):
+    """Append the accepted path (int32 [B, max_path] indices into each sequence's draft) under the
+    sink + recent rule; kv_len_out / cursor_out may be head_kv_len / head_cursor."""
+    import torch
+    _same_device(draft_off=draft_off, path=path, path_len=path_len, k_draft=k_draft, v_draft=v_draft,
+                 k_pages=k_pages, v_pages=v_pages, page_table=page_table, head_page_off=head_page_off,
+                 head_budget=head_budget, head_kv_len=head_kv_len, head_cursor=head_cursor,
+                 kv_len_out=kv_len_out, cursor_out=cursor_out, slot_out=slot_out)
+    B, BH = shape.B, shape.B * shape.Hkv
+    if path.dim() != 2 or path.shape[0] != B:
+        raise ValueError(f"path: shape {tuple(path.shape)}, expected [{B}, max_path]")
+    P, n = path.shape[1], k_draft.shape[0]
+    ks = _tokens(k_draft, "k_draft", shape.Hkv, shape.D)
+    vs = _tokens(v_draft, "v_draft", shape.Hkv, shape.D, n)
+    for name, t, m in (("draft_off", draft_off, B + 1), ("path", path, B * P), ("path_len", path_len, B),
+                       ("page_table", page_table, 0), ("head_budget", head_budget, BH),
+                       ("head_kv_len", head_kv_len, BH), ("head_cursor", head_cursor, BH),
+                       ("kv_len_out", kv_len_out, BH), ("cursor_out", cursor_out, BH),
+                       ("slot_out", slot_out, BH * P)):
+        _need(t, m, torch.int32, name)
+    _need(head_page_off, BH, torch.int64, "head_page_off")
+    _pool(k_pages, shape.num_pages, shape.D, "k_pages")
+    _pool(v_pages, shape.num_pages, shape.D, "v_pages")
+    _check(_lib().tg_append_path_sink_recent(
+        ctypes.byref(shape), int(sink), n, _dp(draft_off), P, _dp(path), _dp(path_len), _dp(k_draft),
+        ks, _dp(v_draft), vs, _dp(k_pages), _dp(v_pages), _dp(page_table), _dp(head_page_off),
+        _dp(head_budget), _dp(head_kv_len), _dp(head_cursor), _dp(kv_len_out), _dp(cursor_out),
+        _dp(slot_out), _stream(stream)), "tg_append_path_sink_recent")
+
+
+def tg_copy_pages(src_page, dst_page, rows, k_pool, v_pool, n_bad, k_scale=None, v_scale=None,
+                  stream=None):
+    """Copy pages src_page[i] -> dst_page[i] (rows[i] rows; None: all 16) within the pools
+    [num_pages, 16, row] (bf16, INT8 or packed INT4), with their scales when given."""
+    import torch
+    _same_device(src_page=src_page, dst_page=dst_page, rows=rows, k_pool=k_pool, v_pool=v_pool,
+                 n_bad=n_bad, k_scale=k_scale, v_scale=v_scale)
+    if k_pool.dim() != 3 or k_pool.shape[1] != 16 or k_pool.shape != v_pool.shape or \
+            k_pool.dtype != v_pool.dtype:
+        raise ValueError("pools: expected two [num_pages, 16, row] tensors of one type")
+    if not (k_pool.is_contiguous() and v_pool.is_contiguous()):
+        raise ValueError("pools: must be contiguous")
+    n, pages = src_page.numel(), k_pool.shape[0]
+    _need(src_page, n, torch.int32, "src_page")
+    if dst_page.numel() != n or (rows is not None and rows.numel() != n):
+        raise ValueError("src_page, dst_page and rows differ in length")
+    _need(dst_page, n, torch.int32, "dst_page")
+    if rows is not None:
+        _need(rows, n, torch.int32, "rows")
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is not None:
+            _need(t, pages * 16, torch.float32, name)
+    _need(n_bad, 1, torch.int32, "n_bad")
+    _check(_lib().tg_copy_pages(pages, k_pool.shape[2] * k_pool.element_size(), n, _dp(src_page),
+                                _dp(dst_page), _dp(rows), _dp(k_pool), _dp(v_pool), _dp(k_scale),
+                                _dp(v_scale), _dp(n_bad), _stream(stream)), "tg_copy_pages")
+
+
+def tg_compact_kv(shape: tg_shape, k_src, v_src, src_table, src_head_off, src_len, keep_off, keep_idx,
+                  k_pages, v_pages, page_table, head_page_off, head_budget, head_kv_len, n_bad,
+                  stream=None):
+    """Compact the kept source tokens of every head into its budget pages (see include/tg.h);
+    k_src / v_src bf16 [src_pages, 16, D]."""
+    import torch
+    _same_device(k_src=k_src, v_src=v_src, src_table=src_table, src_head_off=src_head_off,
+                 src_len=src_len, keep_off=keep_off, keep_idx=keep_idx, k_pages=k_pages,
+                 v_pages=v_pages, page_table=page_table, head_page_off=head_page_off,
+                 head_budget=head_budget, head_kv_len=head_kv_len, n_bad=n_bad)
+    BH = shape.B * shape.Hkv
+    if k_src.dim() != 3 or k_src.shape[1:] != (16, shape.D):
+        raise ValueError(f"k_src: shape {tuple(k_src.shape)}, expected [pages, 16, {shape.D}]")
+    pages, n = k_src.shape[0], keep_idx.numel()
+    _pool(k_src, pages, shape.D, "k_src")
+    _pool(v_src, pages, shape.D, "v_src")
+    _pool(k_pages, shape.num_pages, shape.D, "k_pages")
+    _pool(v_pages, shape.num_pages, shape.D, "v_pages")
+    for name, t, m in (("src_table", src_table, 0), ("src_len", src_len, BH), ("keep_idx", keep_idx, n),
+                       ("page_table", page_table, 0), ("head_budget", head_budget, BH),
+                       ("head_kv_len", head_kv_len, BH), ("n_bad", n_bad, 1)):
+        _need(t, m, torch.int32, name)
+    for name, t, m in (("src_head_off", src_head_off, BH), ("keep_off", keep_off, BH + 1),
+                       ("head_page_off", head_page_off, BH)):
+        _need(t, m, torch.int64, name)
+    _check(_lib().tg_compact_kv(
+        ctypes.byref(shape), pages, _dp(k_src), _dp(v_src), _dp(src_table), _dp(src_head_off),
+        _dp(src_len), _dp(keep_off), _dp(keep_idx), n, _dp(k_pages), _dp(v_pages), _dp(page_table),
+        _dp(head_page_off), _dp(head_budget), _dp(head_kv_len), _dp(n_bad), _stream(stream)),
+        "tg_compact_kv")
 
 
 # ---------------------------------------------------------------------------------------

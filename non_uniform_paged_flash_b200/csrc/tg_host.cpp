@@ -85,6 +85,8 @@ struct tg_alloc {
     struct Seq {
         std::vector<int32_t> priv;    // private pages in allocation order
         std::vector<int32_t> shared;  // shared page references held
+        std::vector<int32_t> pages;   // every head's page list, head after head
+        std::vector<int64_t> start;   // [n_heads + 1] each head's first entry in pages
     };
     std::unordered_map<int32_t, Seq> seqs;
 
@@ -180,11 +182,14 @@ int alloc_reserve(tg_alloc *a, int32_t seq_id, int32_t n_heads, const int32_t *k
     try {
         sq.shared.reserve(static_cast<size_t>(shared_pages) * static_cast<size_t>(n_heads));
         sq.priv.reserve(static_cast<size_t>(priv_total));
+        sq.pages.reserve(static_cast<size_t>(total));
+        sq.start.reserve(static_cast<size_t>(n_heads) + 1);
     } catch (...) {
         a->seqs.erase(seq_id);
         throw;
     }
     int64_t w = 0;
+    sq.start.push_back(0);
     for (int32_t h = 0; h < n_heads; ++h) {
         for (int32_t c = 0; c < n_prefix; ++c) {
             const int32_t s = prefix_segs[c];
@@ -205,7 +210,84 @@ int alloc_reserve(tg_alloc *a, int32_t seq_id, int32_t n_heads, const int32_t *k
             page_ids[w++] = id;
         }
         if (head_count) head_count[h] = static_cast<int32_t>(shared_pages + priv);
+        sq.start.push_back(w);
     }
+    sq.pages.assign(page_ids, page_ids + w);  // within the reserved capacity
+    if (n_written) *n_written = w;
+    return TG_OK;
+}
+
+// Fork: the child's page lists are the parent's first shared_pages[h] pages (one more reference
+// each), then private pages up to the child's length; the parent's pages between those hold rows
+// the child needs its own copies of.
+int alloc_fork(tg_alloc *a, int32_t parent, int32_t child, int32_t n_heads, const int32_t *held, const int32_t *kv_len,
+               const int32_t *shared_pages, int32_t *page_ids, int64_t capacity, int32_t *head_count,
+               int32_t *copy_src, int32_t *copy_dst, int32_t *copy_rows, int64_t copy_capacity, int64_t *n_copies,
+               int64_t *n_written) {
+    if (!a || n_heads < 1 || !held || !kv_len || !shared_pages || capacity < 0 || (capacity > 0 && !page_ids) ||
+        copy_capacity < 0 || (copy_capacity > 0 && (!copy_src || !copy_dst || !copy_rows)) || !n_copies)
+        return TG_EINVAL;
+    const auto it = a->seqs.find(parent);
+    if (it == a->seqs.end()) return TG_ENOTFOUND;
+    if (a->seqs.count(child)) return TG_EEXIST;
+    if (it->second.start.size() != static_cast<size_t>(n_heads) + 1) return TG_EINVAL;
+    int64_t total = 0, priv_total = 0, shared_total = 0, copies = 0;
+    for (int32_t h = 0; h < n_heads; ++h) {
+        const int64_t has = it->second.start[h + 1] - it->second.start[h];
+        const int64_t need = (static_cast<int64_t>(kv_len[h]) + a->page - 1) / a->page;
+        // rows in use fit the parent's pages and the child's length; shared pages are full ones
+        if (held[h] < 0 || kv_len[h] < held[h] || shared_pages[h] < 0 || held[h] > has * a->page ||
+            static_cast<int64_t>(shared_pages[h]) * a->page > held[h])
+            return TG_EINVAL;
+        total += need;
+        priv_total += need - shared_pages[h];
+        shared_total += shared_pages[h];
+        copies += (static_cast<int64_t>(held[h]) + a->page - 1) / a->page - shared_pages[h];
+    }
+    if (total > capacity || copies > copy_capacity) return TG_EINVAL;
+    if (priv_total > a->n_free) return TG_ENOSPC;
+
+    // The fallible steps before any page moves (the new record may rehash the map, so the parent
+    // is looked up again).
+    tg_alloc::Seq &sq = a->seqs[child];
+    try {
+        sq.shared.reserve(static_cast<size_t>(shared_total));
+        sq.priv.reserve(static_cast<size_t>(priv_total));
+        sq.pages.reserve(static_cast<size_t>(total));
+        sq.start.reserve(static_cast<size_t>(n_heads) + 1);
+    } catch (...) {
+        a->seqs.erase(child);
+        throw;
+    }
+    const tg_alloc::Seq &pa = a->seqs.find(parent)->second;
+    int64_t w = 0, c = 0;
+    sq.start.push_back(0);
+    for (int32_t h = 0; h < n_heads; ++h) {
+        const int32_t need = static_cast<int32_t>((static_cast<int64_t>(kv_len[h]) + a->page - 1) / a->page);
+        for (int32_t p = 0; p < need; ++p) {
+            int32_t id;
+            if (p < shared_pages[h]) {
+                id = pa.pages[static_cast<size_t>(pa.start[h] + p)];
+                ++a->refs[id];
+                sq.shared.push_back(id);
+            } else {
+                id = a->take();
+                a->refs[id] = 1;
+                sq.priv.push_back(id);
+                const int64_t rows = static_cast<int64_t>(held[h]) - static_cast<int64_t>(p) * a->page;
+                if (rows > 0) {
+                    copy_src[c] = pa.pages[static_cast<size_t>(pa.start[h] + p)];
+                    copy_dst[c] = id;
+                    copy_rows[c++] = static_cast<int32_t>(std::min<int64_t>(rows, a->page));
+                }
+            }
+            sq.pages.push_back(id);
+            page_ids[w++] = id;
+        }
+        sq.start.push_back(w);
+        if (head_count) head_count[h] = need;
+    }
+    *n_copies = c;
     if (n_written) *n_written = w;
     return TG_OK;
 }
@@ -263,6 +345,34 @@ extern "C" int tg_reserve(tg_alloc *a, int32_t seq_id, int32_t n_heads, const in
         return alloc_reserve(a, seq_id, n_heads, kv_len, n_prefix, prefix_segs, page_ids, capacity,
                              head_count, n_written);
     });
+}
+
+extern "C" int tg_fork(tg_alloc *a, int32_t parent, int32_t child, int32_t n_heads, const int32_t *held,
+                       const int32_t *kv_len, const int32_t *shared_pages, int32_t *page_ids, int64_t capacity,
+                       int32_t *head_count, int32_t *copy_src, int32_t *copy_dst, int32_t *copy_rows,
+                       int64_t copy_capacity, int64_t *n_copies, int64_t *n_written) {
+    return tg::no_throw([&] {
+        return alloc_fork(a, parent, child, n_heads, held, kv_len, shared_pages, page_ids, capacity, head_count,
+                          copy_src, copy_dst, copy_rows, copy_capacity, n_copies, n_written);
+    });
+}
+
+extern "C" int tg_tree_masks(int32_t B, const int32_t *draft_off, const int32_t *parent, uint64_t *mask) {
+    if (B < 0 || !draft_off || (B > 0 && draft_off[0] != 0)) return TG_EINVAL;
+    for (int32_t b = 0; b < B; ++b) {
+        const int64_t n = static_cast<int64_t>(draft_off[b + 1]) - draft_off[b];
+        if (n < 0 || n > TG_MAX_DRAFT || (n > 0 && (!parent || !mask))) return TG_EINVAL;
+        for (int64_t j = 0; j < n; ++j) {
+            const int32_t p = parent[draft_off[b] + j];
+            if (p < -1 || p >= j) return TG_EINVAL;
+        }
+    }
+    for (int32_t b = 0; b < B; ++b)
+        for (int32_t j = 0; j < draft_off[b + 1] - draft_off[b]; ++j) {
+            const int32_t p = parent[draft_off[b] + j];
+            mask[draft_off[b] + j] = (p < 0 ? 0 : mask[draft_off[b] + p]) | (1ull << j);
+        }
+    return TG_OK;
 }
 
 extern "C" int tg_release(tg_alloc *a, int32_t seq_id) {

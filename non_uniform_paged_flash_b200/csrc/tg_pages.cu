@@ -1,0 +1,240 @@
+// Moving retained tokens between pages: page copies (a forked sequence's own copies of pages it
+// will write, a tier copied for a new reader) and the compaction of a prompt's rows to the budget
+// pages of each head.
+//
+// Sources: "Tangram" explainer, 三大机制 1 (Budget Reservation: a head holds only its budget after
+// compression, in pages reserved at admission) and RadixAttention lesson, Phase 17 · 06 (a node's
+// pages are shared until a request departs from them; the partial page is the reader's own).
+//
+// Both kernels only move bytes: each row is read once and written once, 16 bytes a lane.
+#include <cuda_runtime.h>
+#include <climits>
+#include <cstdint>
+
+#include "tg.h"
+#include "tg_internal.h"
+#include "tg_ptx.cuh"
+
+namespace tg {
+namespace {
+
+constexpr int kCopyWarps = 8;
+constexpr int kCopyVec = 8;     // 16-byte vectors of a lane in flight
+constexpr int kCompactWarps = 8;
+
+struct CopyArgs {
+    const int32_t *src, *dst, *rows;
+    int64_t n, num_pages;
+    uint4 *pool[2];
+    float *scale[2];
+    int32_t row_vec;  // 16-byte vectors per row
+    int32_t *n_bad;
+};
+
+// One warp per (pair, K or V): a page's first `rows` rows are one contiguous run of bytes in the
+// pool, copied kCopyVec vectors a lane at a time (a whole bf16 page of D = 128 is one round).
+__global__ void __launch_bounds__(kCopyWarps * 32) copy_pages_kernel(const __grid_constant__ CopyArgs a) {
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const int64_t i = w >> 1;
+    const int side = static_cast<int>(w & 1);
+    ptx::grid_wait();
+    if (i >= a.n) return;
+    const int64_t s = a.src[i], d = a.dst[i];
+    const int32_t rows = a.rows ? a.rows[i] : 16;
+    if (s < 0 || s >= a.num_pages || d < 0 || d >= a.num_pages || rows < 0 || rows > 16) {
+        if (side == 0 && lane == 0) atomicAdd(a.n_bad, 1);
+        return;
+    }
+    if (s == d) return;
+    const int total = rows * a.row_vec;
+    const uint4 *from = a.pool[side] + s * 16 * a.row_vec;
+    uint4 *to = a.pool[side] + d * 16 * a.row_vec;
+    float sc = 0.f;
+    const bool has = a.scale[side] && lane < rows;
+    if (has) sc = a.scale[side][s * 16 + lane];
+    for (int v0 = 0; v0 < total; v0 += 32 * kCopyVec) {
+        uint4 x[kCopyVec];
+#pragma unroll
+        for (int j = 0; j < kCopyVec; ++j)
+            if (v0 + j * 32 + lane < total) x[j] = from[v0 + j * 32 + lane];
+#pragma unroll
+        for (int j = 0; j < kCopyVec; ++j)
+            if (v0 + j * 32 + lane < total) to[v0 + j * 32 + lane] = x[j];
+    }
+    if (has) a.scale[side][d * 16 + lane] = sc;
+}
+
+struct CompactArgs {
+    int32_t BH, row_vec;
+    int64_t n_keep, src_pages, num_pages;
+    const uint4 *k_src, *v_src;
+    uint4 *k_dst, *v_dst;
+    const int32_t *src_table, *table, *src_len, *budget;
+    const int64_t *src_off, *off, *keep_off;
+    const int32_t *keep;
+    int32_t *kv_len, *n_bad;
+};
+
+// Number of rows head bh keeps, or -1 when its list is not usable (out of order, outside keep,
+// longer than its budget).
+__device__ __forceinline__ int64_t kept_rows(const CompactArgs &a, int32_t bh) {
+    const int64_t b = a.keep_off[bh], e = a.keep_off[bh + 1];
+    return b < 0 || e < b || e > a.n_keep || e - b > max(0, a.budget[bh]) ? -1 : e - b;
+}
+
+// One warp per 32 entries of the keep list, whatever heads they belong to, so heads of very
+// different budgets cost the same per row. Lane l finds entry l's head (binary search of
+// keep_off, the same few cached words for every lane), its source and destination rows; then the
+// warp copies the 32 K rows and 32 V rows 16 bytes a lane, the rows' addresses by shuffle.
+__global__ void __launch_bounds__(kCompactWarps * 32) compact_kernel(const __grid_constant__ CompactArgs a) {
+    constexpr unsigned FULL = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    const int64_t gtid = static_cast<int64_t>(blockIdx.x) * (kCompactWarps * 32) + threadIdx.x;
+    ptx::grid_wait();
+    if (gtid < a.BH) {
+        const int64_t m = kept_rows(a, static_cast<int32_t>(gtid));
+        a.kv_len[gtid] = m < 0 ? 0 : static_cast<int32_t>(m);
+        if (m < 0) atomicAdd(a.n_bad, 1);
+    }
+    const int64_t i = (gtid >> 5) * 32 + lane;  // keep-list entry of this lane
+    int64_t src = -1, dst = -1;
+    if (i < a.n_keep) {
+        int32_t lo = 0, hi = a.BH;  // the last head whose list starts at or before i
+        while (hi - lo > 1) {
+            const int32_t mid = (lo + hi) >> 1;
+            if (a.keep_off[mid] <= i) lo = mid;
+            else hi = mid;
+        }
+        const int64_t first = a.keep_off[lo];
+        const int64_t m = kept_rows(a, lo);
+        if (first <= i && i - first < m) {
+            const int64_t to = i - first;
+            const int32_t from = a.keep[i];
+            int64_t sp = -1, dp = a.table[a.off[lo] + to / 16];
+            if (from >= 0 && from < a.src_len[lo]) sp = a.src_table[a.src_off[lo] + from / 16];
+            if (sp >= 0 && sp < a.src_pages && dp >= 0 && dp < a.num_pages) {
+                src = sp * 16 + from % 16;
+                dst = dp * 16 + to % 16;
+            } else {
+                atomicAdd(a.n_bad, 1);
+            }
+        }
+    }
+    if (!__any_sync(FULL, src >= 0)) return;
+    // vector v of the warp's 32 rows: row v / row_vec, K first, then V
+    const int per = 32 * a.row_vec;
+    for (int v0 = 0; v0 < 2 * per; v0 += 32 * kCopyVec) {
+        uint4 x[kCopyVec];
+        uint4 *to[kCopyVec];
+#pragma unroll
+        for (int j = 0; j < kCopyVec; ++j) {
+            const int v = v0 + j * 32 + lane;
+            const bool is_v = v >= per;
+            const int u = is_v ? v - per : v;
+            const int r = u / a.row_vec, c = u - r * a.row_vec;
+            const int64_t s = __shfl_sync(FULL, src, r & 31), d = __shfl_sync(FULL, dst, r & 31);
+            to[j] = nullptr;
+            if (v < 2 * per && s >= 0) {
+                x[j] = (is_v ? a.v_src : a.k_src)[s * a.row_vec + c];
+                to[j] = (is_v ? a.v_dst : a.k_dst) + d * a.row_vec + c;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kCopyVec; ++j)
+            if (to[j]) *to[j] = x[j];
+    }
+}
+
+bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+template <class A>
+int launch(void (*kern)(A), const A &a, int64_t ctas, int threads, tg_stream stream, const char *what) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+    if (e != cudaSuccess) {
+        set_cuda_error(what, static_cast<int>(e));
+        return TG_ECUDA;
+    }
+    return TG_OK;
+}
+
+}  // namespace
+}  // namespace tg
+
+using namespace tg;
+
+extern "C" int tg_copy_pages(int64_t num_pages, int32_t row_bytes, int64_t n_copies, const int32_t *src_page,
+                             const int32_t *dst_page, const int32_t *rows, void *k_pool, void *v_pool, float *k_scale,
+                             float *v_scale, int32_t *n_bad, tg_stream stream) {
+    if (num_pages < 0 || row_bytes < 1 || n_copies < 0 || n_copies > INT32_MAX) return TG_EINVAL;
+    if (row_bytes % 16 != 0 || row_bytes > 4096) return TG_EUNSUPPORTED;
+    if (n_copies == 0) return TG_OK;
+    if (!src_page || !dst_page || !k_pool || !v_pool || !n_bad || !al16(k_pool) || !al16(v_pool) ||
+        !k_scale != !v_scale)
+        return TG_EINVAL;
+    CopyArgs a{};
+    a.src = src_page;
+    a.dst = dst_page;
+    a.rows = rows;
+    a.n = n_copies;
+    a.num_pages = num_pages;
+    a.pool[0] = static_cast<uint4 *>(k_pool);
+    a.pool[1] = static_cast<uint4 *>(v_pool);
+    a.scale[0] = k_scale;
+    a.scale[1] = v_scale;
+    a.row_vec = row_bytes / 16;
+    a.n_bad = n_bad;
+    return launch(copy_pages_kernel, a, (2 * n_copies + kCopyWarps - 1) / kCopyWarps, kCopyWarps * 32, stream,
+                  "copy_pages_kernel");
+}
+
+extern "C" int tg_compact_kv(const tg_shape *s, int64_t src_num_pages, const void *k_src, const void *v_src,
+                             const int32_t *src_table, const int64_t *src_head_off, const int32_t *src_len,
+                             const int64_t *keep_off, const int32_t *keep_idx, int64_t n_keep, void *k_pages,
+                             void *v_pages, const int32_t *page_table, const int64_t *head_page_off,
+                             const int32_t *head_budget, int32_t *head_kv_len, int32_t *n_bad, tg_stream stream) {
+    if (!s || s->B < 0 || s->Hkv < 1 || s->page != 16 || s->D < 8 || s->D % 8 != 0 || s->num_pages < 0 ||
+        static_cast<int64_t>(s->B) * s->Hkv > INT32_MAX || src_num_pages < 0 || n_keep < 0 ||
+        n_keep > static_cast<int64_t>(INT32_MAX) * 64)
+        return TG_EINVAL;
+    if (s->D > 2048) return TG_EUNSUPPORTED;
+    const int32_t BH = s->B * s->Hkv;
+    if (BH == 0) return TG_OK;
+    if (!keep_off || !head_budget || !head_kv_len || !n_bad) return TG_EINVAL;
+    if (n_keep > 0 && (!k_src || !v_src || !src_table || !src_head_off || !src_len || !keep_idx || !k_pages ||
+                       !v_pages || !page_table || !head_page_off))
+        return TG_EINVAL;
+    if (!al16(k_src) || !al16(v_src) || !al16(k_pages) || !al16(v_pages)) return TG_EINVAL;
+    CompactArgs a{};
+    a.BH = BH;
+    a.row_vec = s->D / 8;
+    a.n_keep = n_keep;
+    a.src_pages = src_num_pages;
+    a.num_pages = s->num_pages;
+    a.k_src = static_cast<const uint4 *>(k_src);
+    a.v_src = static_cast<const uint4 *>(v_src);
+    a.k_dst = static_cast<uint4 *>(k_pages);
+    a.v_dst = static_cast<uint4 *>(v_pages);
+    a.src_table = src_table;
+    a.table = page_table;
+    a.src_len = src_len;
+    a.budget = head_budget;
+    a.src_off = src_head_off;
+    a.off = head_page_off;
+    a.keep_off = keep_off;
+    a.keep = keep_idx;
+    a.kv_len = head_kv_len;
+    a.n_bad = n_bad;
+    const int64_t threads = n_keep > BH ? n_keep : BH;
+    return launch(compact_kernel, a, (threads + kCompactWarps * 32 - 1) / (kCompactWarps * 32), kCompactWarps * 32,
+                  stream, "compact_kernel");
+}

@@ -311,6 +311,125 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
     }
 }
 
+// Path append (sink + recent rule, several tokens): the accepted drafted tokens of a sequence,
+// appended in order as append_kernel<0> would one by one. WPH warps per (b, h), a token per warp
+// round: every lane holds two tokens of the path (at most 64), so all slots and page ids of a head
+// are found in one round of loads, and the rows of kPathRound tokens are in flight together.
+//   Token i of m (length n, budget R + s, s sinks, cursor c): the free slot n + i while
+//   n + i < budget, else ring slot s + (c + o) mod R with o = n + i - budget. A later token of the
+//   path replaces it when o + R is still in the path, or, for a free slot s + x, when the ring comes
+//   round to x: (x - c) mod R <= the path's last o. Only the survivor is written, so the order of
+//   the writes does not matter.
+// Lengths and cursors are read before the CTA's barrier and written after it, so the output arrays
+// may be the input arrays. A head whose path names a token outside the draft, or a page outside the
+// pool, is left as it was. Bound: launch and load latency (offsets, page id, row); moves 8 D bytes
+// per accepted token and head.
+constexpr int kPathMax = 64;   // accepted tokens of one sequence at most
+constexpr int kPathRound = 4;  // tokens of a warp in flight
+template <int WPH>
+__global__ void __launch_bounds__(kAppendWarps * 32)
+    append_path_kernel(int32_t BH, int32_t Hkv, int32_t D, int64_t num_pages, int32_t sink, int64_t n_draft,
+                       int32_t P, const int32_t *draft_off, const int32_t *path, const int32_t *path_len,
+                       const uint4 *k_draft, int64_t k_stride, const uint4 *v_draft, int64_t v_stride,
+                       uint4 *k_pages, uint4 *v_pages, const int32_t *table, const int64_t *head_off,
+                       const int32_t *budget, const int32_t *kv_len, const int32_t *cursor,
+                       int32_t *kv_len_out, int32_t *cursor_out, int32_t *slot_out) {
+    constexpr unsigned FULL = 0xffffffffu;
+    constexpr int HEADS = kAppendWarps / WPH;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t bh = blockIdx.x * HEADS + warp / WPH;
+    const int part = warp % WPH;
+    const bool on = bh < BH;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    int32_t n_raw = 0, c_raw = 0, bud = 0, m = 0, slot[2] = {-1, -1};
+    int64_t row[2] = {0, 0}, tok[2] = {0, 0};
+    bool live[2] = {false, false}, bad = false;
+    if (on) {
+        const int32_t b = bh / Hkv;
+        const int64_t t0 = draft_off[b], t1 = draft_off[b + 1], off = head_off[bh];
+        m = path_len[b];
+        bud = budget[bh];
+        n_raw = kv_len[bh];
+        c_raw = cursor[bh];
+        bad = m < 0 || m > P || t0 < 0 || t1 < t0 || t1 > n_draft;
+        if (bad || bud < 1) m = 0;
+        const int32_t s = max(0, min(sink, bud - 1));
+        const int32_t R = max(1, bud - s);
+        const int64_t n = max(0, min(n_raw, bud));
+        int32_t c = c_raw % R;
+        if (c < 0) c += R;
+        const int64_t last = n + m - 1 - bud;  // the path's last ring index (negative: none)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int i = 32 * j + lane;
+            if (i >= m) continue;
+            const int64_t o = n + i - bud;
+            slot[j] = static_cast<int32_t>(o < 0 ? n + i : s + (c + o) % R);
+            live[j] = true;
+            if (o >= 0) {
+                live[j] = o + R > last;
+            } else if (slot[j] >= s && last >= 0) {
+                int32_t d = (slot[j] - s - c) % R;
+                if (d < 0) d += R;
+                live[j] = d > last;
+            }
+            const int32_t rel = path[static_cast<int64_t>(b) * P + i];
+            const int64_t pid = table[off + slot[j] / 16];
+            bad |= rel < 0 || rel >= t1 - t0 || pid < 0 || pid >= num_pages;
+            tok[j] = t0 + rel;
+            row[j] = pid * 16 + slot[j] % 16;
+        }
+    }
+    bad = __any_sync(FULL, bad);
+    const int nvec = D / 8;
+    if (on && !bad) {
+        const int32_t h = bh % Hkv;
+        for (int i0 = part * kPathRound; i0 < m; i0 += WPH * kPathRound) {
+            for (int v0 = 0; v0 < 2 * nvec; v0 += 32) {
+                const int v = v0 + lane;
+                uint4 x[kPathRound];
+                uint4 *to[kPathRound];
+#pragma unroll
+                for (int r = 0; r < kPathRound; ++r) {
+                    const int i = i0 + r;
+                    const int64_t tk = __shfl_sync(FULL, i < 32 ? tok[0] : tok[1], i & 31);
+                    const int64_t rw = __shfl_sync(FULL, i < 32 ? row[0] : row[1], i & 31);
+                    const bool lv = __shfl_sync(FULL, static_cast<int>(i < 32 ? live[0] : live[1]), i & 31) != 0;
+                    to[r] = nullptr;
+                    if (i < m && lv && v < 2 * nvec) {
+                        const bool is_v = v >= nvec;
+                        const int u = is_v ? v - nvec : v;
+                        x[r] = (is_v ? v_draft + tk * v_stride : k_draft + tk * k_stride)[h * nvec + u];
+                        to[r] = (is_v ? v_pages : k_pages) + rw * nvec + u;
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < kPathRound; ++r)
+                    if (to[r]) *to[r] = x[r];
+            }
+        }
+    }
+    __syncthreads();
+    if (!on || part != 0) return;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int i = 32 * j + lane;
+        if (i < P) slot_out[static_cast<int64_t>(bh) * P + i] = !bad && i < m && live[j] ? slot[j] : -1;
+    }
+    if (lane == 0) {
+        const int64_t n = max(0, n_raw);
+        const int32_t s = max(0, min(sink, bud - 1));
+        const int32_t R = max(1, bud - s);
+        const bool moved = !bad && m > 0;
+        kv_len_out[bh] = moved && n_raw < bud ? static_cast<int32_t>(n + m < bud ? n + m : bud) : n_raw;
+        const int64_t over = (n < bud ? n : bud) + m - bud;  // tokens that took ring slots
+        int32_t c = c_raw % R;
+        if (c < 0) c += R;
+        cursor_out[bh] = moved && over > 0 ? static_cast<int32_t>((c + over) % R) : c_raw;
+    }
+}
+
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_shape(const tg_shape *s) {
@@ -354,6 +473,53 @@ extern "C" int tg_append_sink_recent(const tg_shape *shape, int32_t sink, const 
         static_cast<uint4 *>(v_pages), page_table, head_page_off, head_budget, head_kv_len,
         head_cursor, nullptr, nullptr, nullptr, nullptr, slot_out);
     return launch_status("append_kernel<sink+recent>");
+}
+
+extern "C" int tg_append_path_sink_recent(const tg_shape *shape, int32_t sink, int64_t n_draft,
+                                          const int32_t *draft_off, int32_t max_path, const int32_t *path,
+                                          const int32_t *path_len, const void *k_draft, int64_t k_stride,
+                                          const void *v_draft, int64_t v_stride, void *k_pages, void *v_pages,
+                                          const int32_t *page_table, const int64_t *head_page_off,
+                                          const int32_t *head_budget, const int32_t *head_kv_len,
+                                          const int32_t *head_cursor, int32_t *kv_len_out, int32_t *cursor_out,
+                                          int32_t *slot_out, tg_stream stream) {
+    if (check_shape(shape) != TG_OK || sink < 0 || n_draft < 0 || n_draft > INT32_MAX || max_path < 1)
+        return TG_EINVAL;
+    if (max_path > kPathMax) return TG_EUNSUPPORTED;
+    const int32_t BH = shape->B * shape->Hkv;
+    if (BH == 0) return TG_OK;
+    const int64_t width = static_cast<int64_t>(shape->Hkv) * shape->D;
+    if (!draft_off || !path || !path_len || !k_pages || !v_pages || !page_table || !head_page_off || !head_budget ||
+        !head_kv_len || !head_cursor || !kv_len_out || !cursor_out || !slot_out || !al16(k_draft) || !al16(v_draft) ||
+        !al16(k_pages) || !al16(v_pages))
+        return TG_EINVAL;
+    if (n_draft > 0 && (!k_draft || !v_draft || k_stride < width || v_stride < width || k_stride % 8 != 0 ||
+                        v_stride % 8 != 0))
+        return TG_EINVAL;
+    // one warp per head copies kPathRound tokens a round; longer paths get more warps per head
+    const int wph = max_path <= kPathRound ? 1 : max_path <= 2 * kPathRound ? 2 : max_path <= 4 * kPathRound ? 4 : 8;
+    auto kern = wph == 1 ? append_path_kernel<1> : wph == 2 ? append_path_kernel<2>
+              : wph == 4 ? append_path_kernel<4> : append_path_kernel<8>;
+    const int heads = kAppendWarps / wph;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>((BH + heads - 1) / heads));
+    cfg.blockDim = dim3(kAppendWarps * 32);
+    cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(
+        &cfg, kern, BH, shape->Hkv, shape->D, shape->num_pages, sink, n_draft, max_path, draft_off, path, path_len,
+        static_cast<const uint4 *>(k_draft), k_stride / 8, static_cast<const uint4 *>(v_draft), v_stride / 8,
+        static_cast<uint4 *>(k_pages), static_cast<uint4 *>(v_pages), page_table, head_page_off, head_budget,
+        head_kv_len, head_cursor, kv_len_out, cursor_out, slot_out);
+    if (e != cudaSuccess) {
+        set_cuda_error("append_path_kernel", static_cast<int>(e));
+        return TG_ECUDA;
+    }
+    return TG_OK;
 }
 
 extern "C" int tg_append_h2o(const tg_shape *shape, const void *k_new, const void *v_new,
