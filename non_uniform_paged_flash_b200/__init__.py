@@ -247,7 +247,7 @@ def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
-    return torch.cuda.current_stream().cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 # ------------------------------------------------------------------------------------------
@@ -849,29 +849,38 @@ def tg_quantize_int4(src, packed, scale, stream=None):
 # Speculative step and page moves (see include/tg.h).
 # ---------------------------------------------------------------------------------------
 
-def _same_device(**tensors):
-    """Every tensor is on the current CUDA device (the calls launch there)."""
+def _current():
+    """The current CUDA device (these calls launch there); -2, no tensor's device, without one."""
     import torch
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        if not getattr(t, "is_cuda", False):
-            raise ValueError(f"{name}: expected a CUDA tensor")
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError(f"{name}: on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
 
 
-def _tokens(t, what, heads=None, D=None, n=None):
-    """A bf16 [n, heads, D] tensor whose tokens' rows are contiguous: its token stride."""
+def _dev(t, n, dtype, dev, what):
+    """Device pointer of a contiguous tensor of at least n elements of dtype on device dev."""
+    if t.dtype is dtype and t.get_device() == dev and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, n, dtype, what)
+    raise ValueError(f"{what}: on {t.device}, not on the current CUDA device")
+
+
+def _tokens(t, what, heads, D, n, dev):
+    """Device pointer and token stride of a bf16 [n, heads, D] tensor whose tokens' rows are
+    contiguous (heads or n None: any)."""
     import torch
-    if t.dtype != torch.bfloat16 or t.dim() != 3:
+    if t.dtype is not torch.bfloat16 or t.dim() != 3:
         raise ValueError(f"{what}: expected bf16 [tokens, heads, D]")
-    if (heads is not None and t.shape[1] != heads) or (D is not None and t.shape[2] != D) or \
-            (n is not None and t.shape[0] != n):
+    tn, th, td = t.shape
+    if (heads is not None and th != heads) or td != D or (n is not None and tn != n):
         raise ValueError(f"{what}: shape {tuple(t.shape)}, expected [{n}, {heads}, {D}]")
-    if t.numel() and ((t.shape[2] > 1 and t.stride(2) != 1) or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: on {t.device}, not on the current CUDA device")
+    s0, s1, s2 = t.stride()
+    if t.numel() and ((td > 1 and s2 != 1) or (th > 1 and s1 != td)):
         raise ValueError(f"{what}: each token's heads must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return t.data_ptr(), (s0 if tn > 1 else th * td)
 
 
 def tg_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: int = TG_ROPE_NONE,
@@ -892,11 +901,10 @@ def tg_qk_norm_rope(q, k, q_weight, k_weight, eps: float, position, inv_freq, q_
     rot_dim = 2 * inv_freq.numel()."""
     import torch
     side = q if q is not None else k
-    if side is None:
-        raise ValueError("q and k: one must be given")
-    _same_device(q=q, k=k, q_weight=q_weight, k_weight=k_weight, position=position, inv_freq=inv_freq,
-                 q_out=q_out, k_out=k_out)
-    n, _, D = side.shape if side.dim() == 3 else (0, 0, 0)
+    if side is None or side.dim() != 3:
+        raise ValueError("q and k: one must be given, as [tokens, heads, D]")
+    dev = _current()
+    n, _, D = side.shape
     args = []
     for name, x, y, w in (("q", q, q_out, q_weight), ("k", k, k_out, k_weight)):
         if x is None:
@@ -904,19 +912,19 @@ def tg_qk_norm_rope(q, k, q_weight, k_weight, eps: float, position, inv_freq, q_
             continue
         if y is None:
             raise ValueError(f"{name}_out: missing")
-        st = _tokens(x, name, None, D, n)
-        so = _tokens(y, name + "_out", x.shape[1], D, n)
-        if w is not None:
-            _need(w, D, torch.bfloat16, name + "_weight")
-        args.append((x.shape[1], _dp(x), st, _dp(w), _dp(y), so))
+        xp, xs = _tokens(x, name, None, D, n, dev)
+        yp, ys = _tokens(y, name + "_out", x.shape[1], D, n, dev)
+        args.append((x.shape[1], xp, xs, None if w is None else _dev(w, D, torch.bfloat16, dev, name + "_weight"),
+                     yp, ys))
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    fp = pp = None
     if rot and n:
-        _need(inv_freq, rot // 2, torch.float64, "inv_freq")
-        _need(position, n, torch.int32, "position")
+        fp = _dev(inv_freq, rot // 2, torch.float64, dev, "inv_freq")
+        pp = _dev(position, n, torch.int32, dev, "position")
     (Hq, qp, qs, qw, qo, qos), (Hk, kp, ks, kw, ko, kos) = args
-    _check(_lib().tg_qk_norm_rope(n, Hq, Hk, D, qp, qs, kp, ks, qw, kw, float(eps), _dp(position),
-                                  _dp(inv_freq), rot, int(bool(interleaved)), float(rot_scale), qo,
-                                  qos, ko, kos, _stream(stream)), "tg_qk_norm_rope")
+    _check(_lib().tg_qk_norm_rope(n, Hq, Hk, D, qp, qs, kp, ks, qw, kw, float(eps), pp, fp, rot,
+                                  int(bool(interleaved)), float(rot_scale), qo, qos, ko, kos, _stream(stream)),
+           "tg_qk_norm_rope")
 
 
 def tg_tree_masks(draft_off, parent) -> np.ndarray:
@@ -986,10 +994,9 @@ def tg_tree_plan_status(plan: TreePlan, stream=None) -> int:
     return int(_lib().tg_tree_plan_status(plan.handle, _stream(stream)))
 
 
-def _pool(t, pages, D, what):
+def _pool(t, pages, D, dev, what):
     import torch
-    if pages > 0:
-        _need(t, pages * 16 * D, torch.bfloat16, what)
+    return _dev(t, pages * 16 * D, torch.bfloat16, dev, what)
 
 
 def tg_tree_decode(plan: TreePlan, draft_off, q, k_draft, v_draft, tree_mask, k_pages, v_pages,
@@ -998,30 +1005,22 @@ def tg_tree_decode(plan: TreePlan, draft_off, q, k_draft, v_draft, tree_mask, k_
     """Tree attention of drafted tokens (q [n, Hq, D], k_draft / v_draft [n, Hkv, D]) over the cache
     and each other; tree_mask int64 / uint64 [n]."""
     import torch
-    s = plan.shape
-    _same_device(draft_off=draft_off, q=q, k_draft=k_draft, v_draft=v_draft, tree_mask=tree_mask,
-                 k_pages=k_pages, v_pages=v_pages, page_table=page_table, head_page_off=head_page_off,
-                 head_kv_len=head_kv_len, out=out, lse=lse)
+    s, dev = plan.shape, _current()
+    BH, D, i32, i64 = s.B * s.Hkv, s.D, torch.int32, torch.int64
     n = q.shape[0]
-    qs = _tokens(q, "q", s.Hq, s.D)
-    ks = _tokens(k_draft, "k_draft", s.Hkv, s.D, n)
-    vs = _tokens(v_draft, "v_draft", s.Hkv, s.D, n)
-    if tree_mask.dtype not in (torch.int64, torch.uint64):
+    qp, qs = _tokens(q, "q", s.Hq, D, n, dev)
+    kp, ks = _tokens(k_draft, "k_draft", s.Hkv, D, n, dev)
+    vp, vs = _tokens(v_draft, "v_draft", s.Hkv, D, n, dev)
+    if tree_mask.dtype is not i64 and tree_mask.dtype is not torch.uint64:
         raise ValueError(f"tree_mask: expected 64-bit integers, got {tree_mask.dtype}")
-    _need(tree_mask, n, tree_mask.dtype, "tree_mask")
-    _need(draft_off, s.B + 1, torch.int32, "draft_off")
-    _need(head_page_off, s.B * s.Hkv, torch.int64, "head_page_off")
-    _need(head_kv_len, s.B * s.Hkv, torch.int32, "head_kv_len")
-    _need(page_table, 0, torch.int32, "page_table")
-    _pool(k_pages, s.num_pages, s.D, "k_pages")
-    _pool(v_pages, s.num_pages, s.D, "v_pages")
-    _need(out, n * s.Hq * s.D, torch.bfloat16, "out")
-    _need(lse, n * s.Hq, torch.float32, "lse")
     _check(_lib().tg_tree_decode(
-        plan.handle, n, _dp(draft_off), _dp(q), qs, _dp(k_draft), ks, _dp(v_draft), vs,
-        _dp(tree_mask), _dp(k_pages), _dp(v_pages), _dp(page_table), _dp(head_page_off),
-        _dp(head_kv_len), float(scale), float(softcap), _dp(out), _dp(lse), _stream(stream)),
-        "tg_tree_decode")
+        plan.handle, n, _dev(draft_off, s.B + 1, i32, dev, "draft_off"), qp, qs, kp, ks, vp, vs,
+        _dev(tree_mask, n, tree_mask.dtype, dev, "tree_mask"),
+        _pool(k_pages, s.num_pages, D, dev, "k_pages"), _pool(v_pages, s.num_pages, D, dev, "v_pages"),
+        _dev(page_table, 0, i32, dev, "page_table"), _dev(head_page_off, BH, i64, dev, "head_page_off"),
+        _dev(head_kv_len, BH, i32, dev, "head_kv_len"), float(scale), float(softcap),
+        _dev(out, n * s.Hq * D, torch.bfloat16, dev, "out"), _dev(lse, n * s.Hq, torch.float32, dev, "lse"),
+        _stream(stream)), "tg_tree_decode")
 
 
 def tg_append_path_sink_recent(shape: tg_shape, sink: int, draft_off, path, path_len, k_draft, v_draft,
@@ -1030,30 +1029,23 @@ def tg_append_path_sink_recent(shape: tg_shape, sink: int, draft_off, path, path
     """Append the accepted path (int32 [B, max_path] indices into each sequence's draft) under the
     sink + recent rule; kv_len_out / cursor_out may be head_kv_len / head_cursor."""
     import torch
-    _same_device(draft_off=draft_off, path=path, path_len=path_len, k_draft=k_draft, v_draft=v_draft,
-                 k_pages=k_pages, v_pages=v_pages, page_table=page_table, head_page_off=head_page_off,
-                 head_budget=head_budget, head_kv_len=head_kv_len, head_cursor=head_cursor,
-                 kv_len_out=kv_len_out, cursor_out=cursor_out, slot_out=slot_out)
-    B, BH = shape.B, shape.B * shape.Hkv
+    dev, i32 = _current(), torch.int32
+    B, Hkv, D = shape.B, shape.Hkv, shape.D
+    BH = B * Hkv
     if path.dim() != 2 or path.shape[0] != B:
         raise ValueError(f"path: shape {tuple(path.shape)}, expected [{B}, max_path]")
     P, n = path.shape[1], k_draft.shape[0]
-    ks = _tokens(k_draft, "k_draft", shape.Hkv, shape.D)
-    vs = _tokens(v_draft, "v_draft", shape.Hkv, shape.D, n)
-    for name, t, m in (("draft_off", draft_off, B + 1), ("path", path, B * P), ("path_len", path_len, B),
-                       ("page_table", page_table, 0), ("head_budget", head_budget, BH),
-                       ("head_kv_len", head_kv_len, BH), ("head_cursor", head_cursor, BH),
-                       ("kv_len_out", kv_len_out, BH), ("cursor_out", cursor_out, BH),
-                       ("slot_out", slot_out, BH * P)):
-        _need(t, m, torch.int32, name)
-    _need(head_page_off, BH, torch.int64, "head_page_off")
-    _pool(k_pages, shape.num_pages, shape.D, "k_pages")
-    _pool(v_pages, shape.num_pages, shape.D, "v_pages")
+    kp, ks = _tokens(k_draft, "k_draft", Hkv, D, n, dev)
+    vp, vs = _tokens(v_draft, "v_draft", Hkv, D, n, dev)
     _check(_lib().tg_append_path_sink_recent(
-        ctypes.byref(shape), int(sink), n, _dp(draft_off), P, _dp(path), _dp(path_len), _dp(k_draft),
-        ks, _dp(v_draft), vs, _dp(k_pages), _dp(v_pages), _dp(page_table), _dp(head_page_off),
-        _dp(head_budget), _dp(head_kv_len), _dp(head_cursor), _dp(kv_len_out), _dp(cursor_out),
-        _dp(slot_out), _stream(stream)), "tg_append_path_sink_recent")
+        ctypes.byref(shape), int(sink), n, _dev(draft_off, B + 1, i32, dev, "draft_off"), P,
+        _dev(path, B * P, i32, dev, "path"), _dev(path_len, B, i32, dev, "path_len"), kp, ks, vp, vs,
+        _pool(k_pages, shape.num_pages, D, dev, "k_pages"), _pool(v_pages, shape.num_pages, D, dev, "v_pages"),
+        _dev(page_table, 0, i32, dev, "page_table"), _dev(head_page_off, BH, torch.int64, dev, "head_page_off"),
+        _dev(head_budget, BH, i32, dev, "head_budget"), _dev(head_kv_len, BH, i32, dev, "head_kv_len"),
+        _dev(head_cursor, BH, i32, dev, "head_cursor"), _dev(kv_len_out, BH, i32, dev, "kv_len_out"),
+        _dev(cursor_out, BH, i32, dev, "cursor_out"), _dev(slot_out, BH * P, i32, dev, "slot_out"),
+        _stream(stream)), "tg_append_path_sink_recent")
 
 
 def tg_copy_pages(src_page, dst_page, rows, k_pool, v_pool, n_bad, k_scale=None, v_scale=None,
@@ -1061,27 +1053,22 @@ def tg_copy_pages(src_page, dst_page, rows, k_pool, v_pool, n_bad, k_scale=None,
     """Copy pages src_page[i] -> dst_page[i] (rows[i] rows; None: all 16) within the pools
     [num_pages, 16, row] (bf16, INT8 or packed INT4), with their scales when given."""
     import torch
-    _same_device(src_page=src_page, dst_page=dst_page, rows=rows, k_pool=k_pool, v_pool=v_pool,
-                 n_bad=n_bad, k_scale=k_scale, v_scale=v_scale)
-    if k_pool.dim() != 3 or k_pool.shape[1] != 16 or k_pool.shape != v_pool.shape or \
-            k_pool.dtype != v_pool.dtype:
+    dev, i32 = _current(), torch.int32
+    if k_pool.dim() != 3 or k_pool.shape[1] != 16 or k_pool.shape != v_pool.shape:
         raise ValueError("pools: expected two [num_pages, 16, row] tensors of one type")
-    if not (k_pool.is_contiguous() and v_pool.is_contiguous()):
-        raise ValueError("pools: must be contiguous")
-    n, pages = src_page.numel(), k_pool.shape[0]
-    _need(src_page, n, torch.int32, "src_page")
+    pages, _, row = k_pool.shape
+    n = src_page.numel()
     if dst_page.numel() != n or (rows is not None and rows.numel() != n):
         raise ValueError("src_page, dst_page and rows differ in length")
-    _need(dst_page, n, torch.int32, "dst_page")
-    if rows is not None:
-        _need(rows, n, torch.int32, "rows")
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t is not None:
-            _need(t, pages * 16, torch.float32, name)
-    _need(n_bad, 1, torch.int32, "n_bad")
-    _check(_lib().tg_copy_pages(pages, k_pool.shape[2] * k_pool.element_size(), n, _dp(src_page),
-                                _dp(dst_page), _dp(rows), _dp(k_pool), _dp(v_pool), _dp(k_scale),
-                                _dp(v_scale), _dp(n_bad), _stream(stream)), "tg_copy_pages")
+    kp = _dev(k_pool, 0, k_pool.dtype, dev, "k_pool")
+    vp = _dev(v_pool, 0, k_pool.dtype, dev, "v_pool")
+    f32 = torch.float32
+    _check(_lib().tg_copy_pages(
+        pages, row * k_pool.element_size(), n, _dev(src_page, n, i32, dev, "src_page"),
+        _dev(dst_page, n, i32, dev, "dst_page"), None if rows is None else _dev(rows, n, i32, dev, "rows"), kp, vp,
+        None if k_scale is None else _dev(k_scale, pages * 16, f32, dev, "k_scale"),
+        None if v_scale is None else _dev(v_scale, pages * 16, f32, dev, "v_scale"),
+        _dev(n_bad, 1, i32, dev, "n_bad"), _stream(stream)), "tg_copy_pages")
 
 
 def tg_compact_kv(shape: tg_shape, k_src, v_src, src_table, src_head_off, src_len, keep_off, keep_idx,
@@ -1090,29 +1077,19 @@ def tg_compact_kv(shape: tg_shape, k_src, v_src, src_table, src_head_off, src_le
     """Compact the kept source tokens of every head into its budget pages (see include/tg.h);
     k_src / v_src bf16 [src_pages, 16, D]."""
     import torch
-    _same_device(k_src=k_src, v_src=v_src, src_table=src_table, src_head_off=src_head_off,
-                 src_len=src_len, keep_off=keep_off, keep_idx=keep_idx, k_pages=k_pages,
-                 v_pages=v_pages, page_table=page_table, head_page_off=head_page_off,
-                 head_budget=head_budget, head_kv_len=head_kv_len, n_bad=n_bad)
-    BH = shape.B * shape.Hkv
-    if k_src.dim() != 3 or k_src.shape[1:] != (16, shape.D):
-        raise ValueError(f"k_src: shape {tuple(k_src.shape)}, expected [pages, 16, {shape.D}]")
+    dev, i32, i64 = _current(), torch.int32, torch.int64
+    BH, D = shape.B * shape.Hkv, shape.D
+    if k_src.dim() != 3 or k_src.shape[1] != 16 or k_src.shape[2] != D:
+        raise ValueError(f"k_src: shape {tuple(k_src.shape)}, expected [pages, 16, {D}]")
     pages, n = k_src.shape[0], keep_idx.numel()
-    _pool(k_src, pages, shape.D, "k_src")
-    _pool(v_src, pages, shape.D, "v_src")
-    _pool(k_pages, shape.num_pages, shape.D, "k_pages")
-    _pool(v_pages, shape.num_pages, shape.D, "v_pages")
-    for name, t, m in (("src_table", src_table, 0), ("src_len", src_len, BH), ("keep_idx", keep_idx, n),
-                       ("page_table", page_table, 0), ("head_budget", head_budget, BH),
-                       ("head_kv_len", head_kv_len, BH), ("n_bad", n_bad, 1)):
-        _need(t, m, torch.int32, name)
-    for name, t, m in (("src_head_off", src_head_off, BH), ("keep_off", keep_off, BH + 1),
-                       ("head_page_off", head_page_off, BH)):
-        _need(t, m, torch.int64, name)
     _check(_lib().tg_compact_kv(
-        ctypes.byref(shape), pages, _dp(k_src), _dp(v_src), _dp(src_table), _dp(src_head_off),
-        _dp(src_len), _dp(keep_off), _dp(keep_idx), n, _dp(k_pages), _dp(v_pages), _dp(page_table),
-        _dp(head_page_off), _dp(head_budget), _dp(head_kv_len), _dp(n_bad), _stream(stream)),
+        ctypes.byref(shape), pages, _pool(k_src, pages, D, dev, "k_src"), _pool(v_src, pages, D, dev, "v_src"),
+        _dev(src_table, 0, i32, dev, "src_table"), _dev(src_head_off, BH, i64, dev, "src_head_off"),
+        _dev(src_len, BH, i32, dev, "src_len"), _dev(keep_off, BH + 1, i64, dev, "keep_off"),
+        _dev(keep_idx, n, i32, dev, "keep_idx"), n, _pool(k_pages, shape.num_pages, D, dev, "k_pages"),
+        _pool(v_pages, shape.num_pages, D, dev, "v_pages"), _dev(page_table, 0, i32, dev, "page_table"),
+        _dev(head_page_off, BH, i64, dev, "head_page_off"), _dev(head_budget, BH, i32, dev, "head_budget"),
+        _dev(head_kv_len, BH, i32, dev, "head_kv_len"), _dev(n_bad, 1, i32, dev, "n_bad"), _stream(stream)),
         "tg_compact_kv")
 
 

@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <memory>
@@ -40,7 +41,7 @@ static_assert(sizeof(TreeItem) == 32, "TreeItem is 32 bytes");
 
 // A block of query rows whose head is split over nsplit >= 2 consecutive slots.
 struct TreeMerge {
-    int32_t bh, first_slot, nsplit, row0, cap, pad[3];
+    int32_t bh, first_slot, nsplit, row0;
 };
 
 }  // namespace tg
@@ -54,11 +55,13 @@ struct tg_tree_plan {
     int32_t n_workers = 0;
     int32_t rows_item = 0;   // query rows of an item at most
     int32_t q_rows = 0;      // rows of one Q box (multiple of 8)
+    int32_t q_boxes = 1;     // Q boxes in shared memory
+    int32_t entries = 0;     // K / V ring entries
+    int32_t smem_bytes = 0;
     int32_t n_slots = 0;
-    std::vector<tg::TreeItem> items;
+    std::vector<tg::TreeItem> items;      // each worker's items, then the dynamic ones
     std::vector<int32_t> worker_off;
     std::vector<tg::TreeMerge> merge;
-    std::vector<int32_t> slot_page;  // first page of each slot's item
     std::vector<int64_t> row_lo, row_hi;  // bounds of each KV head's group table
 
     void *dev_base = nullptr;
@@ -66,10 +69,9 @@ struct tg_tree_plan {
     tg::TreeItem *d_items = nullptr;
     int32_t *d_worker_off = nullptr;
     tg::TreeMerge *d_merge = nullptr;
-    int32_t *d_slot_page = nullptr;
     int64_t *d_row_lo = nullptr, *d_row_hi = nullptr;
     float *d_part_o = nullptr, *d_part_lse = nullptr;
-    uint32_t *d_err = nullptr;
+    uint32_t *d_err = nullptr, *d_ticket = nullptr;  // d_ticket: next dynamic item, CTAs done
 };
 
 namespace tg {
@@ -78,6 +80,7 @@ namespace {
 constexpr int kRows = 128;      // rows of a tile = tensor-memory lanes
 constexpr int kBlock = 64;      // tokens of a block (4 pages)
 constexpr int kHdr = 16;        // block headers kept
+constexpr int kMaxEntries = 24; // ring entries at most: a header outlives its block (see the kernel)
 constexpr int kCutPages = 4;    // heads are cut at whole blocks
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -85,44 +88,48 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // Block header flags.
 constexpr int32_t kFirst = 1, kLast = 2, kDraft = 4, kStop = 8;
 
+// What the block's consumers need to know, written by the producer before the block's K arrives.
 struct alignas(16) BlockHdr {
-    int32_t flags;
-    int32_t nv;     // valid tokens of the block
-    int32_t nrow;   // valid query rows of the item
-    int32_t bh;
+    int32_t flags;  // | valid tokens << 8 | valid query rows of the item << 16
     int32_t tok0;   // the sequence's first drafted token
-    int32_t row0;
-    int32_t slot;
-    int32_t pad;
+    int32_t h;      // KV head
+    int32_t slot;   // partial-result slot or -1
+    int32_t row0;   // first query row of the item
+    int16_t qb;     // the item's Q box
+    int16_t v_fill; // ring fill (modulo 2 entries) that brings the block's V
     unsigned long long bad;  // drafted tokens whose V row holds an infinity or NaN
-    unsigned long long pad2;
 };
-static_assert(sizeof(BlockHdr) == 48, "BlockHdr layout");
+static_assert(sizeof(BlockHdr) == 32, "BlockHdr layout");
 
+// Shared memory: Q boxes (q_rows query rows each, per tile), the K / V ring, block headers, barriers.
 template <int D, int TILES>
 struct TreeLayout {
     static constexpr int kHalves = D / 64;             // 128-byte column halves
     static constexpr int kEntry = kBlock * D * 2;      // K or V of a block
-    static constexpr int kQTile = kRows * D * 2;
-    static constexpr int kEntries = TILES == 1 ? (D == 128 ? 5 : 10) : (D == 128 ? 9 : 20);
-    static constexpr int kQ = 0;
-    static constexpr int kRing = TILES * kQTile;
-    static constexpr int kHdrs = kRing + kEntries * kEntry;
-    static constexpr int kBars = kHdrs + kHdr * static_cast<int>(sizeof(BlockHdr));
+    static constexpr int kGroup = 1024 * kHalves;      // 8 tokens of it: a swizzled atom per half
     // full[E], empty[E], q_full[2], q_empty[2], per tile: s_full[2], p_full[2], o_done[2], drain
-    static constexpr int kNumBars = 2 * kEntries + 4 + 7 * TILES;
-    static constexpr int kBytes = kBars + 8 * kNumBars + 16;
+    static constexpr int kControl = kHdr * static_cast<int>(sizeof(BlockHdr)) + 8 * (2 * kMaxEntries + 4 + 7 * TILES) + 16;
+    // one CTA of two tiles, or two CTAs of one tile, per SM (228 KB, 1 KB of it reserved per CTA)
+    static constexpr int kLimit = TILES == 1 ? (228 * 1024) / 2 - 1024 : 227 * 1024;
     static constexpr int kThreads = 32 * (5 * TILES + 1);
     static constexpr uint32_t kCols = 256u * TILES;    // tensor-memory columns
+    static int q_bytes(int q_rows, int boxes) { return (boxes * TILES * q_rows * D * 2 + 1023) / 1024 * 1024; }
+    static int entries(int q_rows, int boxes) {
+        return std::min(kMaxEntries, (kLimit - q_bytes(q_rows, boxes) - kControl) / kEntry);
+    }
 };
 
 struct TreeArgs {
     const TreeItem *items;
     const int32_t *worker_off;
-    int32_t G, Hq, Hkv, max_draft, q_rows, rows_item;
+    int32_t n_items;
+    int32_t G, g_shift, Hq, Hkv, max_draft, q_rows, rows_item;
+    int32_t q_boxes, entries, ring;  // ring: offset of the K / V ring in shared memory
     int64_t n_tokens, num_pages;
     float scale_log2;       // scale * log2 e
-    float cap2, cap_in;     // softcap * log2 e; 2 log2 e * scale / softcap
+    float cap2;             // softcap * log2 e
+    float cap_x, cap_x_signed;  // |scale| / softcap, scale / softcap
+    float cap_p[4];         // cap2 tanh(cap_x_signed s) = s (p0 + p1 s^2 + ...) for small s
     const __nv_bfloat16 *v_draft;
     int64_t v_stride;
     const unsigned long long *mask;
@@ -133,7 +140,7 @@ struct TreeArgs {
     __nv_bfloat16 *out;
     float *lse;
     float *part_o, *part_lse;
-    uint32_t *err;
+    uint32_t *err, *ticket;
     uint64_t wait_ns;
 };
 
@@ -149,8 +156,9 @@ __device__ __forceinline__ bool any_nonfinite(uint32_t w) {  // two bf16: an exp
 }
 
 // ------------------------------------------------------------------------------------------
-// Tree kernel: a persistent CTA per worker walks the worker's items (equal shares of the reserved
-// pages, cut ahead of time). Per CTA and tile of 128 query rows:
+// Tree kernel: a persistent CTA per worker walks the worker's items (equal shares of most of the
+// reserved pages, cut ahead of time), then items of the rest by ticket, which evens out what the
+// SMs' different memory rates leave. Per CTA and tile of 128 query rows:
 //   warps 0-3 (and 4-7):  softmax; thread i owns query row i = tensor-memory lane i, so a row's
 //                         max and sum need no shuffles
 //   one warp per tile:    MMA issue (lane 0)
@@ -170,6 +178,15 @@ __device__ __forceinline__ bool any_nonfinite(uint32_t w) {  // two bf16: an exp
 // tokens are zeroed in shared memory before the product (0 * NaN); and an infinity or NaN in a
 // drafted V row is taken out of the product and added back only for the rows that attend to it.
 // ------------------------------------------------------------------------------------------
+
+// tanh on |x| <= kTanhNear as x p(x^2), p of degree 3 fitted for the least maximum relative error
+// (Lawson's reweighted least squares; 9.8e-08 in exact arithmetic). Scores of a capped head are mostly
+// this small, and five multiplications and additions on pairs of scores cost less than the general
+// form's two special-function calls each (three with the exponential, on a quarter-rate unit that
+// bounds wide drafts). The host folds the scales into the coefficients.
+constexpr float kTanhNear = 0.4f;
+constexpr double kTanh[4] = {0.999999901901, -0.333313624587, 0.132709767556, -0.0475536034831};
+
 template <int D, int TILES, bool CAP>
 __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2 : 1)
     tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap tm_q,
@@ -178,22 +195,23 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
     using TL = TreeLayout<D, TILES>;
     using namespace ptx;
     constexpr unsigned FULL = 0xffffffffu;
-    constexpr int NE = TL::kEntries;
     constexpr int KS = D / 16;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = smem_addr(smem);
-    BlockHdr *hdrs = reinterpret_cast<BlockHdr *>(smem + TL::kHdrs);
-    const uint32_t bar0 = sbase + TL::kBars;
-    const uint32_t full = bar0, empty = bar0 + 8 * NE, q_full = bar0 + 16 * NE, q_empty = q_full + 16;
+    const int NE = a.entries;
+    const uint32_t ring = sbase + a.ring;
+    unsigned char *control = smem + a.ring + NE * TL::kEntry;
+    BlockHdr *hdrs = reinterpret_cast<BlockHdr *>(control);
+    const uint32_t full = smem_addr(control) + kHdr * static_cast<uint32_t>(sizeof(BlockHdr));
+    const uint32_t empty = full + 8 * kMaxEntries, q_full = empty + 8 * kMaxEntries, q_empty = q_full + 16;
     const uint32_t s_full = q_empty + 16, p_full = s_full + 16 * TILES, o_done = p_full + 16 * TILES,
                    drain = o_done + 16 * TILES;
-    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(smem + TL::kBars + 8 * TL::kNumBars);
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(control + TL::kControl - 16);
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // Q of the next item is loaded beside the current one's when two boxes fit
-    const int nq = TILES == 1 && a.q_rows <= kRows / 2 ? 2 : 1;
-    const uint32_t q_half = static_cast<uint32_t>(a.q_rows) * 128u;      // bytes of one column half of a box
-    const uint32_t q_box = q_half * TL::kHalves;
+    const int nq = a.q_boxes;
+    const uint32_t q_half = static_cast<uint32_t>(a.q_rows) * 128u;  // bytes of one column half of a box
+    const uint32_t q_tile = q_half * TL::kHalves;                    // one tile's part of a box
 
     if (threadIdx.x == 0) {
         for (int e = 0; e < NE; ++e) {
@@ -211,13 +229,21 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
         }
         for (int t = 0; t < TILES; ++t) mbar_init(drain + 8 * t, 1);
         *abort_flag = (sbase & 1023u) ? 1 : 0;  // swizzled tiles need 1024-byte alignment
-        if (sbase & 1023u) atomicOr(a.err, kErrPlan);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 4 * TILES) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(smem_addr(const_cast<uint32_t *>(tmem_slot))), "r"(TL::kCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // the plan's own lists do not change between calls: read before the preceding kernel is done
+    int32_t i0 = 0, i1 = 0, n_static = 0;
+    TreeItem first{};
+    if (warp == 5 * TILES) {
+        i0 = a.worker_off[blockIdx.x];
+        i1 = a.worker_off[blockIdx.x + 1];
+        n_static = a.worker_off[gridDim.x];
+        if (i0 < i1) first = a.items[i0];
     }
     fence_before();
     __syncthreads();
@@ -232,32 +258,48 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
 
     if (warp == 5 * TILES) {
         // ================================ producer warp ================================
-        const int32_t i0 = a.worker_off[blockIdx.x], i1 = a.worker_off[blockIdx.x + 1];
-        auto fetch = [&](int32_t i) {
+        auto state_of = [&](const TreeItem &it) {
             ItemState s;
-            s.it = a.items[i];
-            const int32_t b = s.it.bh / a.Hkv;
+            s.it = it;
+            const int32_t b = it.bh / a.Hkv;
             s.tok0 = a.draft_off[b];
             s.nb = a.draft_off[b + 1] - s.tok0;
-            s.len = a.kv_len[s.it.bh];
-            s.off = a.head_off[s.it.bh];
+            s.len = a.kv_len[it.bh];
+            s.off = a.head_off[it.bh];
             return s;
         };
+        // the item after i of this worker: its own list, then tickets; -1 at the end
+        auto after = [&](int32_t i) {
+            if (i + 1 < i1) return i + 1;
+            if (n_static >= a.n_items) return -1;
+            int32_t k = 0;
+            if (lane == 0) k = static_cast<int32_t>(atomicAdd(a.ticket, 1u));
+            k = n_static + __shfl_sync(FULL, k, 0);
+            if (k >= a.n_items) return -1;
+            i1 = 0;  // from here on by ticket
+            return k;
+        };
+        int32_t cur = i0 < i1 ? i0 : after(i1 - 1);
         ItemState nx{};
-        if (i0 < i1) nx = fetch(i0);
-        int32_t blk = 0, qn = 0, entries = 0;
+        if (cur >= 0) nx = state_of(i0 < i1 ? first : a.items[cur]);
+        int32_t ent = 0, blk = 0, qn = 0, fills = 0;
+        uint32_t eph = 1u;  // parity that says entry `ent` is free
         bool stop = *abort_flag != 0;
-        auto wait_entry = [&](int32_t e) {
+        if (stop && lane == 0) atomicOr(a.err, kErrPlan);
+        auto wait_entry = [&]() {
             int32_t bad = 0;
-            if (lane == 0 && (!mbar_wait(empty + 8 * (e % NE), (static_cast<uint32_t>(e / NE) & 1u) ^ 1u, a.wait_ns) || *abort_flag)) {
+            if (lane == 0 && !mbar_wait(empty + 8 * ent, eph, a.wait_ns, abort_flag)) {
                 timed_out();
                 bad = 1;
             }
             return __shfl_sync(FULL, bad, 0) == 0;
         };
-        for (int32_t i = i0; i < i1 && !stop; ++i) {
-            ItemState s = nx;
-            if (i + 1 < i1) nx = fetch(i + 1);
+        auto advance = [&]() {
+            cur = after(cur);
+            if (cur >= 0) nx = state_of(a.items[cur]);
+        };
+        while (cur >= 0 && !stop) {
+            const ItemState s = nx;
             const int32_t b = s.it.bh / a.Hkv, h = s.it.bh - b * a.Hkv;
             // a bad sequence or head is skipped whole: nothing of it is read
             uint32_t err = 0;
@@ -267,19 +309,53 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
             if (!err && pages > 0 && (s.off < a.row_lo[h] || s.off + pages > a.row_hi[h])) err |= kErrBadRow;
             if (err) {
                 if (lane == 0) atomicOr(a.err, err);
+                advance();
                 continue;
             }
             const int32_t nrow = min(s.nb * a.G - s.it.row0, a.rows_item);
-            if (nrow <= 0) continue;
+            if (nrow <= 0) {
+                advance();
+                continue;
+            }
             const int32_t np = max(0, min(s.it.page_end, pages) - s.it.page_begin);
             const int32_t nc = (np + 3) / 4, nblk = nc + s.it.draft;
-            if (nblk == 0) continue;
+            if (nblk == 0) {  // a part of a growing head that holds nothing yet
+                for (int32_t r = lane; r < nrow; r += 32)
+                    a.part_lse[static_cast<int64_t>(s.it.slot) * a.rows_item + r] = -INFINITY;
+                advance();
+                continue;
+            }
+            // the next item is looked up while this one's blocks are in flight; a ticket is drawn late,
+            // so that it is not held back from a CTA that is done earlier
+            const int32_t look = cur + 1 < i1 ? 0 : max(0, nblk - 2);
             const int32_t *row = a.table + s.off + s.it.page_begin;
             int32_t ids = lane < np ? __ldg(row + lane) : -1;
             int32_t ids_next = 32 + lane < np ? __ldg(row + 32 + lane) : -1;
+            const int qb = nq == 2 ? (qn & 1) : 0;
+            // Fills go in the order of use: K(0), then K(j) and V(j - 1), then V of the last block.
+            int32_t pid = 0, p_pid = 0, boxes = 0, p_boxes = 0;
+            bool is_draft = false, p_draft = false;
+            auto fill = [&](bool is_v, bool draft, int32_t page, int32_t n16) {
+                const uint32_t fb = full + 8 * ent;
+                if (lane == 0) mbar_expect_tx(fb, static_cast<uint32_t>(n16) * 16u * D * 2u);
+                __syncwarp();
+                if (lane < (draft ? 2 * n16 : n16)) {
+                    const uint32_t dst = ring + ent * TL::kEntry;
+                    if (draft) tma_4d(dst + lane * TL::kGroup, is_v ? &tm_vd : &tm_kd, 0, s.tok0 + 8 * lane, 0, h, fb);
+                    else tma_4d(dst + lane * 2 * TL::kGroup, is_v ? &tm_v : &tm_k, 0, 0, 0, page * 2, fb);
+                }
+                ++fills;
+                if (++ent == NE) {
+                    ent = 0;
+                    eph ^= 1u;
+                }
+            };
             for (int32_t j = 0; j < nblk && !stop; ++j, ++blk) {
-                const bool is_draft = j == nc;
-                int32_t nv, boxes;
+                p_pid = pid;
+                p_boxes = boxes;
+                p_draft = is_draft;
+                is_draft = j == nc;
+                int32_t nv;
                 if (is_draft) {
                     nv = s.nb;
                     boxes = (nv + 15) / 16;
@@ -291,157 +367,170 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
                         ids_next = 4 * j + 32 + lane < np ? __ldg(row + 4 * j + 32 + lane) : -1;
                     }
                 }
-                // lane 2 p + half loads half-page p of K, then of V
-                const int pg = lane >> 1, hf = lane & 1;
-                int64_t pid = is_draft ? 0 : __shfl_sync(FULL, ids, (4 * j + (pg & 3)) & 31);
-                const bool mine = pg < boxes && hf < TL::kHalves && lane < 8;
-                if (!is_draft && mine && (pid < 0 || pid >= a.num_pages)) {
+                // lane p loads page p of K, later of V; of the draft, 8 tokens
+                pid = is_draft ? 0 : __shfl_sync(FULL, ids, (4 * j + (lane & 3)) & 31);
+                if (!is_draft && lane < boxes && (pid < 0 || pid >= a.num_pages)) {
                     atomicOr(a.err, kErrBadPage);
                     pid = 0;  // a page of the pool; the row is flagged as unspecified
                 }
-                const uint32_t bytes = static_cast<uint32_t>(boxes) * 16u * D * 2u;
-                const int32_t y = is_draft ? s.tok0 + 16 * pg : static_cast<int32_t>(pid * 16);
-                for (int kv = 0; kv < 2; ++kv) {
-                    const int32_t e = 2 * blk + kv;
-                    if (!wait_entry(e)) {
-                        stop = true;
-                        break;
-                    }
-                    const uint32_t fb = full + 8 * (e % NE);
-                    if (lane == 0) {
-                        if (kv == 0) {
-                            BlockHdr *hd = hdrs + (blk % kHdr);
-                            hd->flags = (j == 0 ? kFirst : 0) | (j == nblk - 1 ? kLast : 0) | (is_draft ? kDraft : 0);
-                            hd->nv = nv;
-                            hd->nrow = nrow;
-                            hd->bh = s.it.bh;
-                            hd->tok0 = s.tok0;
-                            hd->row0 = s.it.row0;
-                            hd->slot = s.it.slot;
-                            hd->bad = 0ull;
-                        }
-                        mbar_expect_tx(fb, bytes);
-                    }
-                    __syncwarp();
-                    if (mine) {
-                        const uint32_t dst = sbase + TL::kRing + (e % NE) * TL::kEntry + hf * (kBlock * 128) + pg * 2048;
-                        if (is_draft) tma_3d(dst, kv ? &tm_vd : &tm_kd, hf * 64, h, y, fb);
-                        else tma_2d(dst, kv ? &tm_v : &tm_k, hf * 64, y, fb);
-                    }
-                    __syncwarp();
-                    entries = e + 1;
+                const bool last = j == nblk - 1;
+                if (!wait_entry()) {
+                    stop = true;
+                    break;
                 }
-                if (j == 0 && !stop) {
-                    // the item's query rows, into the box that the item before last has left
-                    const int qb = qn % nq;
+                if (lane == 0) {
+                    BlockHdr *hd = hdrs + (blk % kHdr);
+                    hd->flags = (j == 0 ? kFirst : 0) | (last ? kLast : 0) | (is_draft ? kDraft : 0) | (nv << 8) | (nrow << 16);
+                    hd->tok0 = s.tok0;
+                    hd->h = h;
+                    hd->slot = s.it.slot;
+                    hd->row0 = s.it.row0;
+                    hd->qb = static_cast<int16_t>(qb);
+                    hd->v_fill = static_cast<int16_t>((fills + 1 + (j > 0) + !last) % (2 * NE));
+                    hd->bad = 0ull;
+                }
+                fill(false, is_draft, pid, boxes);
+                if (j == 0) {
+                    // the item's query rows, into a box whose last scores are done
                     int32_t bad = 0;
                     if (lane == 0) {
-                        if (!mbar_wait(q_empty + 8 * qb, (static_cast<uint32_t>(qn / nq) & 1u) ^ 1u, a.wait_ns) || *abort_flag) {
+                        if (!mbar_wait(q_empty + 8 * qb, (static_cast<uint32_t>(qn / nq) & 1u) ^ 1u, a.wait_ns, abort_flag)) {
                             timed_out();
                             bad = 1;
                         } else {
-                            mbar_expect_tx(q_full + 8 * qb, q_box * TILES);
+                            mbar_expect_tx(q_full + 8 * qb, q_tile * TILES);
 #pragma unroll
                             for (int t = 0; t < TILES; ++t)
 #pragma unroll
                                 for (int qh = 0; qh < TL::kHalves; ++qh)
-                                    tma_3d(sbase + TL::kQ + t * TL::kQTile + qb * q_box + qh * q_half, &tm_q, qh * 64, h * a.G,
-                                           s.tok0 + (s.it.row0 + t * kRows) / a.G, q_full + 8 * qb);
+                                    tma_3d(sbase + (qb * TILES + t) * q_tile + qh * q_half, &tm_q, qh * 64, h * a.G,
+                                           s.tok0 + ((s.it.row0 + t * kRows) >> a.g_shift), q_full + 8 * qb);
                         }
                     }
-                    if (__shfl_sync(FULL, bad, 0)) stop = true;
-                    else ++qn;
+                    if (__shfl_sync(FULL, bad, 0)) {
+                        stop = true;
+                        break;
+                    }
+                    ++qn;
+                } else {
+                    if (!wait_entry()) {
+                        stop = true;
+                        break;
+                    }
+                    fill(true, p_draft, p_pid, p_boxes);
                 }
+                if (j == look) advance();
+            }
+            if (!stop) {
+                if (wait_entry()) fill(true, is_draft, pid, boxes);
+                else stop = true;
             }
         }
-        const bool ended = !stop && wait_entry(2 * blk);
-        if (ended) {  // the end marker, in the entry that the oldest copy has left
-            if (lane == 0) {
-                hdrs[blk % kHdr].flags = kStop;
-                mbar_arrive(full + 8 * ((2 * blk) % NE));
-            }
+        const bool ended = !stop && wait_entry();
+        if (ended && lane == 0) {  // the end marker, in the entry that the oldest copy has left
+            hdrs[blk % kHdr].flags = kStop;
+            mbar_arrive(full + 8 * ent);
         }
-        // no copy may be in flight when the CTA exits
-        const uint64_t lim = a.wait_ns < kDrainNs ? a.wait_ns : kDrainNs;
         if (lane == 0) {
-            for (int32_t e = max(0, entries - NE + (ended ? 1 : 0)); e < entries; ++e)
-                mbar_wait(full + 8 * (e % NE), static_cast<uint32_t>(e / NE) & 1u, lim);
+            // no copy may be in flight when the CTA exits
+            const uint64_t lim = a.wait_ns < kDrainNs ? a.wait_ns : kDrainNs;
+            for (int32_t f = max(0, fills - NE + (ended ? 1 : 0)); f < fills; ++f)
+                mbar_wait(full + 8 * (f % NE), static_cast<uint32_t>(f / NE) & 1u, lim);
             for (int32_t k = max(0, qn - nq); k < qn; ++k)
                 mbar_wait(q_full + 8 * (k % nq), static_cast<uint32_t>(k / nq) & 1u, lim);
+            // the last CTA to come here readies the tickets for the next call
+            if (n_static < a.n_items && atomicAdd(a.ticket + 1, 1u) == gridDim.x - 1) {
+                a.ticket[0] = 0u;
+                a.ticket[1] = 0u;
+            }
         }
         __syncwarp();
     } else if (warp >= 4 * TILES) {
         // ================================ MMA warps ================================
         // S(blk) is issued before PV(blk - 1), so the next scores are ready when the softmax has
         // finished a block. P(blk) lies over S(blk) in its buffer; S(blk + 2), which reuses it, is
-        // issued by this thread after PV(blk), and the MMAs of one thread run in issue order.
+        // issued by this thread after PV(blk), and the MMAs of one thread run in issue order. One
+        // thread's instructions are the longest chain of a block when little else is to do, so
+        // addresses are sums and waits that have passed cost one test.
         const int t = warp - 4 * TILES;
         if (lane == 0) {
+            constexpr uint32_t hi_q = sdesc_hi(1024), hi_kv = sdesc_hi(TL::kGroup);
             constexpr uint32_t id_s = idesc_bf16(kBlock, kRows, 0), id_o = idesc_bf16(D, kRows, 1);
             const uint32_t tm = tmem + 256 * t, t_o = tm + 128;
+            const uint32_t k_lo = sdesc_lo(ring, 16), v_lo = sdesc_lo(ring, 1024), q_lo = sdesc_lo(sbase, 16) + ((t * q_tile) >> 4);
             bool ok = *abort_flag == 0;
-            int32_t qn = 0;
-            int32_t p_flags = 0, p_nv = 0;
+            int32_t qn = 0, ent = 0;  // the ring's entries come in the order of use
+            uint32_t eph = 0u;
+            int32_t p_info = 0;
             bool p_on = false;
-            for (int32_t blk = 0; ok; ++blk) {
-                const int32_t e = 2 * blk;
-                ok = mbar_wait(full + 8 * (e % NE), static_cast<uint32_t>(e / NE) & 1u, a.wait_ns) && !*abort_flag;
-                if (!ok) break;
+            auto next_entry = [&]() {
+                if (++ent == NE) {
+                    ent = 0;
+                    eph ^= 1u;
+                }
+            };
+            auto pv = [&](int32_t blk) {  // O += P V of block blk - 1
+                const uint32_t pf = (blk & 1) ^ 1u;
+                if (!mbar_wait(full + 8 * ent, eph, a.wait_ns, abort_flag) ||
+                    !mbar_wait(p_full + 8 * (2 * t + pf), static_cast<uint32_t>((blk - 1) >> 1) & 1u, a.wait_ns, abort_flag))
+                    return false;
                 fence_after();
-                const volatile BlockHdr *hd = hdrs + (blk % kHdr);
-                const int32_t flags = hd->flags, nv = hd->nv;
-                const bool on = !(flags & kStop) && hd->nrow > t * kRows;
-                if (!(flags & kStop)) {
-                    const int qb = qn % nq;
-                    if (flags & kFirst) {
-                        ok = mbar_wait(q_full + 8 * qb, static_cast<uint32_t>(qn / nq) & 1u, a.wait_ns) && !*abort_flag;
-                        if (!ok) break;
-                        fence_after();
-                    }
-                    if (on) {
-                        const uint32_t q = sbase + TL::kQ + t * TL::kQTile + qb * q_box;
-                        const uint32_t k = sbase + TL::kRing + (e % NE) * TL::kEntry;
+                if (p_on) {
+                    const uint32_t v = v_lo + ent * (TL::kEntry >> 4), pa = tm + 64 * pf;
+                    const int nk = (((p_info >> 8) & 0xFF) + 15) >> 4;
+                    mma_ts(t_o, pa, v, hi_kv, id_o, !(p_info & kFirst));
 #pragma unroll
-                        for (int ks = 0; ks < KS; ++ks) {
-                            const uint32_t hf = ks / 4, o = (ks % 4) * 32;
-                            mma_ss(tm + 64 * (blk & 1), sdesc(q + hf * q_half + o, 16, 1024),
-                                   sdesc(k + hf * (kBlock * 128) + o, 16, 1024), id_s, ks > 0);
-                        }
-                        mma_commit(s_full + 8 * (2 * t + (blk & 1)));
-                        mma_commit(empty + 8 * (e % NE));
-                        if (flags & kLast) mma_commit(q_empty + 8 * qb);
-                    } else {
-                        mbar_arrive(s_full + 8 * (2 * t + (blk & 1)));
-                        mbar_arrive(empty + 8 * (e % NE));
-                        if (flags & kLast) mbar_arrive(q_empty + 8 * qb);
-                    }
-                    if (flags & kLast) ++qn;
+                    for (int k = 1; k < 4; ++k)
+                        if (k < nk) mma_ts(t_o, pa + 8 * k, v + k * (2 * TL::kGroup >> 4), hi_kv, id_o, 1);
+                    mma_commit(o_done + 8 * (2 * t + pf));
+                    mma_commit(empty + 8 * ent);
+                } else {
+                    mbar_arrive(o_done + 8 * (2 * t + pf));
+                    mbar_arrive(empty + 8 * ent);
                 }
-                if (blk > 0) {
-                    const int32_t pb = blk - 1, pe = 2 * pb + 1;
-                    ok = mbar_wait(p_full + 8 * (2 * t + (pb & 1)), static_cast<uint32_t>(pb >> 1) & 1u, a.wait_ns) &&
-                         mbar_wait(full + 8 * (pe % NE), static_cast<uint32_t>(pe / NE) & 1u, a.wait_ns) && !*abort_flag;
-                    if (!ok) break;
+                next_entry();
+                return true;
+            };
+            for (int32_t blk = 0; ok; ++blk) {
+                const uint32_t bf = blk & 1;
+                // The header comes with the block's K, which follows the last item's last V: at a change
+                // of items that V is the next entry.
+                if (p_info & kLast) {
+                    if (!(ok = pv(blk))) break;
+                }
+                ok = mbar_wait(full + 8 * ent, eph, a.wait_ns, abort_flag);
+                if (!ok) break;
+                const volatile BlockHdr *hd = hdrs + (blk % kHdr);
+                const int32_t info = hd->flags;
+                const bool on = (info >> 16) > t * kRows;
+                if (!(info & kStop)) {
+                    if (info & kFirst) {
+                        ok = mbar_wait(q_full + 8 * hd->qb, static_cast<uint32_t>(qn / nq) & 1u, a.wait_ns, abort_flag);
+                        if (!ok) break;
+                        ++qn;
+                    }
                     fence_after();
-                    if (p_on) {
-                        const uint32_t v = sbase + TL::kRing + (pe % NE) * TL::kEntry;
-                        const int nk = (p_nv + 15) / 16;
-                        for (int k = 0; k < nk; ++k)
-                            mma_ts(t_o, tm + 64 * (pb & 1) + 8 * k, sdesc(v + k * 2048, kBlock * 128, 1024), id_o,
-                                   k > 0 || !(p_flags & kFirst));
-                        mma_commit(o_done + 8 * (2 * t + (pb & 1)));
-                        mma_commit(empty + 8 * (pe % NE));
+                    if (on) {
+                        const uint32_t q = q_lo + ((hd->qb * TILES * q_tile) >> 4), k = k_lo + ent * (TL::kEntry >> 4);
+#pragma unroll
+                        for (int ks = 0; ks < KS; ++ks)
+                            mma_ss(tm + 64 * bf, q + (ks / 4) * (q_half >> 4) + (ks % 4) * 2, hi_q,
+                                   k + (ks / 4) * (1024 >> 4) + (ks % 4) * 2, hi_kv, id_s, ks > 0);
+                        mma_commit(s_full + 8 * (2 * t + bf));
+                        mma_commit(empty + 8 * ent);
+                        if (info & kLast) mma_commit(q_empty + 8 * hd->qb);
                     } else {
-                        mbar_arrive(o_done + 8 * (2 * t + (pb & 1)));
-                        mbar_arrive(empty + 8 * (pe % NE));
+                        mbar_arrive(s_full + 8 * (2 * t + bf));
+                        mbar_arrive(empty + 8 * ent);
+                        if (info & kLast) mbar_arrive(q_empty + 8 * hd->qb);
                     }
-                }
-                if (flags & kStop) {
-                    mbar_arrive(s_full + 8 * (2 * t + (blk & 1)));
+                } else {
+                    mbar_arrive(s_full + 8 * (2 * t + bf));
                     break;
                 }
-                p_flags = flags;
-                p_nv = nv;
+                next_entry();
+                if (!(info & kFirst) && !(ok = pv(blk))) break;
+                p_info = info;
                 p_on = on;
             }
             if (!ok) timed_out();
@@ -453,7 +542,8 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
     } else {
         // ================================ softmax warps ================================
         const int t = warp >> 2, qd = warp & 3;
-        const int i = kRows * t + 32 * qd + lane;  // row of the item
+        const int w0 = kRows * t + 32 * qd;        // the warp's first row of the item
+        const int i = w0 + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
         const uint32_t t_s = tmem + lanes + 256 * t, t_o = t_s + 128;
         float m = -INFINITY, le = 0.f;
@@ -461,48 +551,50 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
         bool ok = *abort_flag == 0;
         for (int32_t blk = 0; ok; ++blk) {
             const int bf = blk & 1;
-            ok = mbar_wait(s_full + 8 * (2 * t + bf), static_cast<uint32_t>(blk >> 1) & 1u, a.wait_ns) && !*abort_flag;
+            ok = mbar_wait(s_full + 8 * (2 * t + bf), static_cast<uint32_t>(blk >> 1) & 1u, a.wait_ns, abort_flag);
             if (!__all_sync(FULL, ok)) { ok = false; break; }
             fence_after();
             BlockHdr *hd = hdrs + (blk % kHdr);
             const volatile BlockHdr *vh = hd;
-            const int32_t flags = vh->flags;
-            if (flags & kStop) break;
-            const int32_t nv = vh->nv, nrow = vh->nrow;
+            const int32_t info = vh->flags;
+            if (info & kStop) break;
+            const int32_t nv = (info >> 8) & 0xFF, nrow = info >> 16;
             const bool valid = i < nrow;
-            if (kRows * t + 32 * qd >= nrow) {  // no row of this warp
+            if (w0 >= nrow) {  // no row of this warp
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * (2 * t + bf));
                 continue;
             }
-            if (flags & kFirst) {
+            uint32_t sr[64];
+            tmem_ld64(t_s + 64 * bf, sr);
+            if (info & kFirst) {
                 m = -INFINITY;
                 le = 0.f;
-                mask = valid ? __ldg(a.mask + vh->tok0 + (vh->row0 + i) / a.G) : 0ull;
+                mask = valid ? __ldg(a.mask + vh->tok0 + ((vh->row0 + i) >> a.g_shift)) : 0ull;
             }
             // places of this block that count: the valid tokens; of the draft, those of the mask
             unsigned long long sees = nv >= 64 ? ~0ull : (1ull << nv) - 1ull;
-            if (flags & kDraft) sees &= mask;
+            if (info & kDraft) sees &= mask;
             // V rows between the valid tokens and the end of their 16-row box: zeros (stale rows may
             // hold NaN, which a zero probability does not silence); an infinity or NaN in a drafted
             // V row leaves the product too (added back below for the rows that see it)
-            if (qd == 0 && ((nv & 15) || (flags & kDraft))) {
-                const int32_t ve = 2 * blk + 1;
-                ok = mbar_wait(full + 8 * (ve % NE), static_cast<uint32_t>(ve / NE) & 1u, a.wait_ns) && !*abort_flag;
+            if (qd == 0 && ((nv & 15) || (info & kDraft))) {
+                const int32_t v_fill = vh->v_fill, v_ent = v_fill >= NE ? v_fill - NE : v_fill;
+                ok = mbar_wait(full + 8 * v_ent, v_fill >= NE, a.wait_ns, abort_flag);
                 if (!__all_sync(FULL, ok)) { ok = false; break; }
-                const uint32_t v = sbase + TL::kRing + (ve % NE) * TL::kEntry;
+                const uint32_t v = ring + v_ent * TL::kEntry;
                 const int32_t end = (nv + 15) & ~15;
                 for (int32_t c = lane; c < (end - nv) * 8 * TL::kHalves; c += 32) {
                     const int32_t r = nv + c / (8 * TL::kHalves), q = c % (8 * TL::kHalves);
                     asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
-                                 ::"r"(v + (q >> 3) * (kBlock * 128) + r * 128 + (q & 7) * 16), "r"(0u) : "memory");
+                                 ::"r"(v + (r >> 3) * TL::kGroup + (q >> 3) * 1024 + (r & 7) * 128 + (q & 7) * 16), "r"(0u) : "memory");
                 }
-                if (flags & kDraft) {
+                if (info & kDraft) {
                     for (int32_t r = lane; r < nv; r += 32) {
                         uint32_t seen = 0u;
 #pragma unroll
                         for (int q = 0; q < 8 * TL::kHalves; ++q) {
-                            const uint32_t addr = v + (q >> 3) * (kBlock * 128) + r * 128 + (((q & 7) ^ (r & 7)) << 4);
+                            const uint32_t addr = v + (r >> 3) * TL::kGroup + (q >> 3) * 1024 + (r & 7) * 128 + (((q & 7) ^ (r & 7)) << 4);
                             uint4 x;
                             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                                          : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr) : "memory");
@@ -513,7 +605,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
                             __threadfence_block();
                             for (int q = 0; q < 8 * TL::kHalves; ++q)
                                 if (seen >> q & 1u) {
-                                    const uint32_t addr = v + (q >> 3) * (kBlock * 128) + r * 128 + (((q & 7) ^ (r & 7)) << 4);
+                                    const uint32_t addr = v + (r >> 3) * TL::kGroup + (q >> 3) * 1024 + (r & 7) * 128 + (((q & 7) ^ (r & 7)) << 4);
                                     for (int w = 0; w < 8; ++w) {
                                         uint16_t x;
                                         asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(addr + 2 * w) : "memory");
@@ -527,27 +619,44 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
                 fence_async_smem();
                 __syncwarp();
             }
-            uint32_t sr[64];
-            tmem_ld64(t_s + 64 * bf, sr);
             tmem_wait_ld();
-            if (CAP) {
-                // c tanh(x) in log2 units, tanh(x) = 1 - 2 / (1 + 2^(2 x log2 e)): absolute error of
-                // a few 2^-24 c, and the limits +-c at the ends
-#pragma unroll
-                for (int c = 0; c < 64; ++c) {
-                    const float e = ex2(__uint_as_float(sr[c]) * a.cap_in);
-                    sr[c] = __float_as_uint(a.cap2 * fmaf(-2.f, rcp(1.f + e), 1.f));
-                }
-            }
             float sl2 = CAP ? 1.f : a.scale_log2;
-            const bool whole = sees == ~0ull;
-            const bool all_whole = __all_sync(FULL, whole);
-            float mr[8];
+            if (CAP) {
+                // c tanh(x) in log2 units, x = s scale / c
+                float far = 0.f;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) mr[c] = -INFINITY;
-            if (!all_whole) {
+                for (int c = 0; c < 64; c += 2)
+                    far = max3(far, fabsf(__uint_as_float(sr[c])), fabsf(__uint_as_float(sr[c + 1])));
+                if (__all_sync(FULL, far * a.cap_x <= kTanhNear)) {
+                    const f2 c0 = pair(a.cap_p[0], a.cap_p[0]), c1 = pair(a.cap_p[1], a.cap_p[1]),
+                             c2 = pair(a.cap_p[2], a.cap_p[2]), c3 = pair(a.cap_p[3], a.cap_p[3]);
+#pragma unroll
+                    for (int c = 0; c < 64; c += 2) {
+                        const f2 x = pair(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+                        const f2 y = mul2(x, x);
+                        const f2 p = mul2(x, fma2(fma2(fma2(c3, y, c2), y, c1), y, c0));
+                        float u, w;
+                        split(p, u, w);
+                        sr[c] = __float_as_uint(u);
+                        sr[c + 1] = __float_as_uint(w);
+                    }
+                } else {
+                    // tanh(x) = 1 - 2 / (1 + e^2x): absolute error of a few 2^-24 c, limits +-c
+                    const float k2 = 2.f * kLog2e * a.cap_x_signed;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) {
+                        const float e = ex2(__uint_as_float(sr[c]) * k2);
+                        sr[c] = __float_as_uint(a.cap2 * fmaf(-2.f, rcp(1.f + e), 1.f));
+                    }
+                }
+            } else if (sl2 < 0.f) {  // the maximum below is of the products: turn them under a negative scale
+#pragma unroll
+                for (int c = 0; c < 64; ++c) sr[c] ^= 0x80000000u;
+                sl2 = -sl2;
+            }
+            if (!__all_sync(FULL, sees == ~0ull)) {
                 // a score that does not count becomes -inf, so that its probability is zero; the
-                // scale goes in first (it may be zero or negative)
+                // scale goes in first (it may be zero)
                 const uint32_t lo = static_cast<uint32_t>(sees), hi = static_cast<uint32_t>(sees >> 32);
 #pragma unroll
                 for (int c = 0; c < 64; ++c) {
@@ -556,17 +665,20 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
                 }
                 sl2 = 1.f;
             }
+            float mr[4];
 #pragma unroll
-            for (int c = 0; c < 64; ++c) mr[c & 7] = fmaxf(mr[c & 7], __uint_as_float(sr[c]) * sl2);
-            const float mx = fmaxf(fmaxf(fmaxf(mr[0], mr[1]), fmaxf(mr[2], mr[3])),
-                                   fmaxf(fmaxf(mr[4], mr[5]), fmaxf(mr[6], mr[7])));
+            for (int c = 0; c < 4; ++c) mr[c] = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 64; c += 2)
+                mr[(c >> 1) & 3] = max3(mr[(c >> 1) & 3], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+            const float mx = max3(fmaxf(mr[0], mr[1]), mr[2], mr[3]) * sl2;
             const bool up = mx > m + 8.f;
             if (__any_sync(FULL, up)) {
                 const float mn = up ? mx : m;
                 const float c0 = !up ? 1.f : (m == -INFINITY ? 0.f : ex2(m - mn));
-                if (!(flags & kFirst)) {
+                if (!(info & kFirst)) {
                     // O holds the products up to PV(blk - 1): wait for it, then scale in place
-                    ok = mbar_wait(o_done + 8 * (2 * t + (bf ^ 1)), static_cast<uint32_t>((blk - 1) >> 1) & 1u, a.wait_ns) && !*abort_flag;
+                    ok = mbar_wait(o_done + 8 * (2 * t + (bf ^ 1)), static_cast<uint32_t>((blk - 1) >> 1) & 1u, a.wait_ns, abort_flag);
                     if (!__all_sync(FULL, ok)) { ok = false; break; }
                     fence_after();
 #pragma unroll 1
@@ -583,71 +695,95 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
                 le *= c0;
                 m = mn;
             }
-            // p = 2^(s - m), bf16 for the product (its operand type; half a step is 2^-9 of p), fp32
+            // p = 2^(s - m), bf16 for the product (its operand type; half a step is 2^-8 of p), fp32
             // for the sum; m stays -inf while nothing counted: p = 0 then
             const float nm = m == -INFINITY ? 0.f : -m;
-            float ls[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            const f2 nm2 = pair(nm, nm), sc2 = pair(sl2, sl2);
+            f2 ls[4] = {pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f)};
             uint32_t pw[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-                const float p0 = ex2(fmaf(__uint_as_float(sr[2 * e]), sl2, nm));
-                const float p1 = ex2(fmaf(__uint_as_float(sr[2 * e + 1]), sl2, nm));
-                ls[e & 3] += p0;
-                ls[4 + (e & 3)] += p1;
+                float p0, p1;
+                split(fma2(pair(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), sc2, nm2), p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                ls[e & 3] = add2(ls[e & 3], pair(p0, p1));
                 pw[e] = pack_bf16(p0, p1);
             }
-            le += ((ls[0] + ls[1]) + (ls[2] + ls[3])) + ((ls[4] + ls[5]) + (ls[6] + ls[7]));
             tmem_st32(t_s + 64 * bf, pw);
+            {
+                float u, w;
+                split(add2(add2(ls[0], ls[1]), add2(ls[2], ls[3])), u, w);
+                le += u + w;
+            }
             tmem_wait_st();
             fence_before();
             __syncwarp();
-            const int32_t tok0 = vh->tok0, bh = vh->bh, slot = vh->slot, row0 = vh->row0;
             if (lane == 0) mbar_arrive(p_full + 8 * (2 * t + bf));
-            if (!(flags & kLast)) continue;
+            if (!(info & kLast)) continue;
 
             // ---- the item's rows: out = O / le, lse = (m + log2 le) ln 2 ----
-            ok = mbar_wait(o_done + 8 * (2 * t + bf), static_cast<uint32_t>(blk >> 1) & 1u, a.wait_ns) && !*abort_flag;
+            const int32_t tok0 = vh->tok0, h = vh->h, slot = vh->slot, row0 = vh->row0;
+            ok = mbar_wait(o_done + 8 * (2 * t + bf), static_cast<uint32_t>(blk >> 1) & 1u, a.wait_ns, abort_flag);
             if (!__all_sync(FULL, ok)) { ok = false; break; }
             fence_after();
             const float inv = le > 0.f ? 1.f / le : (le == 0.f ? 0.f : le);
-            const unsigned long long bad = (flags & kDraft) ? *const_cast<volatile unsigned long long *>(&hd->bad) & sees : 0ull;
-            const int32_t b = bh / a.Hkv, h = bh - b * a.Hkv, r = row0 + i;
-            const int64_t orow = valid ? (static_cast<int64_t>(tok0 + r / a.G) * a.Hq + h * a.G + r % a.G) : 0;
+            const unsigned long long bad = (info & kDraft) ? *const_cast<volatile unsigned long long *>(&hd->bad) & sees : 0ull;
+            // The rows leave 16 at a time in the fragment that puts 4 lanes on 32 bytes of a row, so
+            // that a store instruction writes whole sectors of 8 rows and not 16 bytes of 32.
+            const bool fin = slot < 0;
+            auto row_of = [&](int32_t rr) {  // final output row of the item's row rr
+                const int32_t r = row0 + rr;
+                return static_cast<int64_t>(tok0 + (r >> a.g_shift)) * a.Hq + h * a.G + (r & (a.G - 1));
+            };
+            const bool any_bad = __any_sync(FULL, bad != 0ull);
 #pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) {
-                uint32_t o[32];
-                tmem_ld32(t_o + 32 * ch, o);
-                tmem_wait_ld();
-                float f[32];
+            for (int r16 = 0; r16 < 32 && w0 + r16 < nrow; r16 += 16) {
+                const int32_t ra = w0 + r16 + (lane >> 2), rb = ra + 8;  // this thread's two rows
+                const float ia = __shfl_sync(FULL, inv, r16 + (lane >> 2)), ib = __shfl_sync(FULL, inv, r16 + (lane >> 2) + 8);
+                const bool va = ra < nrow, vb = rb < nrow;
+                const int c0 = 2 * (lane & 3);
+                const int64_t oa = va ? row_of(ra) * D + c0 : 0, ob = vb ? row_of(rb) * D + c0 : 0;
+                float *pa = fin ? nullptr : a.part_o + (static_cast<int64_t>(slot) * a.rows_item + ra) * D + c0;
 #pragma unroll
-                for (int c = 0; c < 32; ++c) f[c] = __uint_as_float(o[c]) * inv;
-                if (bad) {
-                    for (unsigned long long left = bad; left; left &= left - 1) {
-                        const int j = __ffsll(static_cast<long long>(left)) - 1;
-                        const __nv_bfloat16 *vr = a.v_draft + (static_cast<int64_t>(tok0) + j) * a.v_stride + h * D + 32 * ch;
+                for (int half = 0; half < TL::kHalves; ++half) {
+                    uint32_t o[32];
+                    tmem_ld_16x64(t_o + (static_cast<uint32_t>(r16) << 16) + 64 * half, o);
+                    tmem_wait_ld();
+                    float f[32];
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const float x = __bfloat162float(vr[c]);
-                            if (!isfinite(x)) f[c] += x;
+                    for (int c = 0; c < 32; ++c) f[c] = __uint_as_float(o[c]) * (c & 2 ? ib : ia);
+                    if (any_bad) {
+#pragma unroll
+                        for (int side = 0; side < 2; ++side) {
+                            unsigned long long rest = __shfl_sync(FULL, bad, r16 + (lane >> 2) + 8 * side);
+                            for (; rest; rest &= rest - 1) {
+                                const int j = __ffsll(static_cast<long long>(rest)) - 1;
+                                const __nv_bfloat16 *vr = a.v_draft + (static_cast<int64_t>(tok0) + j) * a.v_stride + h * D + 64 * half + c0;
+#pragma unroll
+                                for (int k = 0; k < 16; ++k) {
+                                    const float x = __bfloat162float(vr[8 * (k >> 1) + (k & 1)]);
+                                    if (!isfinite(x)) f[4 * (k >> 1) + 2 * side + (k & 1)] += x;
+                                }
+                            }
                         }
                     }
-                }
-                if (!valid) continue;
-                if (slot < 0) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(a.out + orow * D + 32 * ch);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        dst[c] = make_uint4(pack_bf16(f[8 * c], f[8 * c + 1]), pack_bf16(f[8 * c + 2], f[8 * c + 3]),
-                                            pack_bf16(f[8 * c + 4], f[8 * c + 5]), pack_bf16(f[8 * c + 6], f[8 * c + 7]));
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(a.part_o + (static_cast<int64_t>(slot) * a.rows_item + i) * D + 32 * ch);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) dst[c] = make_float4(f[4 * c], f[4 * c + 1], f[4 * c + 2], f[4 * c + 3]);
+                    for (int k = 0; k < 8; ++k) {
+                        const int at = 64 * half + 8 * k;
+                        if (fin) {
+                            if (va) *reinterpret_cast<uint32_t *>(a.out + oa + at) = pack_bf16(f[4 * k], f[4 * k + 1]);
+                            if (vb) *reinterpret_cast<uint32_t *>(a.out + ob + at) = pack_bf16(f[4 * k + 2], f[4 * k + 3]);
+                        } else {
+                            if (va) *reinterpret_cast<float2 *>(pa + at) = make_float2(f[4 * k], f[4 * k + 1]);
+                            if (vb) *reinterpret_cast<float2 *>(pa + 8 * D + at) = make_float2(f[4 * k + 2], f[4 * k + 3]);
+                        }
+                    }
                 }
             }
             if (valid) {
                 const float l = le == 0.f ? -INFINITY : (m + lg2(le)) * kLn2;
-                if (slot < 0) a.lse[orow] = l;
+                if (fin) a.lse[row_of(i)] = l;
                 else a.part_lse[static_cast<int64_t>(slot) * a.rows_item + i] = l;
             }
             fence_before();
@@ -663,13 +799,14 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
 }
 
 // ------------------------------------------------------------------------------------------
-// Merge of the split heads: a warp per query row, its parts in order (page ranges ascending), by
-// log-sum-exp. A part whose pages hold no token yet was not written and is left out; the last part
-// holds the drafted tokens and always counts.
+// Merge of the split heads: a warp per query row, by log-sum-exp over its parts in order (page
+// ranges ascending; a part that holds nothing has lse -inf). Lane j weighs part j; the parts'
+// loads do not wait for one another. Bound: one round of loads from L2, where the parts were just
+// written.
 // ------------------------------------------------------------------------------------------
 struct TreeMergeArgs {
     const TreeMerge *merge;
-    const int32_t *slot_page, *draft_off, *kv_len;
+    const int32_t *draft_off;
     int32_t G, Hq, Hkv, max_draft, rows_item;
     int64_t n_tokens;
     const float *part_o, *part_lse;
@@ -677,37 +814,65 @@ struct TreeMergeArgs {
     float *lse;
 };
 constexpr int kMergeWarps = 8;
+constexpr int kMergeParts = 4;  // parts of a row in flight
 
 template <int D>
 __global__ void __launch_bounds__(kMergeWarps * 32) tree_merge_kernel(const __grid_constant__ TreeMergeArgs a) {
     constexpr int E = D / 32;  // elements per lane
-    ptx::grid_wait();
-    ptx::grid_launch();
-    const TreeMerge mg = a.merge[blockIdx.x];
+    constexpr unsigned FULL = 0xffffffffu;
+    const TreeMerge mg = a.merge[blockIdx.x];  // the plan's own list
     const int lane = threadIdx.x & 31;
     const int32_t i = blockIdx.y * kMergeWarps + (threadIdx.x >> 5);
     const int32_t b = mg.bh / a.Hkv, h = mg.bh - b * a.Hkv;
-    const int32_t tok0 = a.draft_off[b], nb = a.draft_off[b + 1] - tok0, len = a.kv_len[mg.bh];
-    if (nb < 0 || nb > a.max_draft || tok0 < 0 || static_cast<int64_t>(tok0) + nb > a.n_tokens || len < 0 || len > mg.cap) return;
-    const int32_t r = mg.row0 + i;
-    if (i >= a.rows_item || r >= nb * a.G) return;
-    const int32_t pages = (len + 15) / 16;
+    ptx::grid_wait();
+    ptx::grid_launch();
+    if (i >= a.rows_item) return;
+    const int32_t tok0 = a.draft_off[b], nb = a.draft_off[b + 1] - tok0;
+    const float *pl = a.part_lse + static_cast<int64_t>(mg.first_slot) * a.rows_item + i;
+    const float *po = a.part_o + (static_cast<int64_t>(mg.first_slot) * a.rows_item + i) * D + lane * E;
+    const int64_t step = static_cast<int64_t>(a.rows_item) * D;
     float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int32_t j = 0; j < mg.nsplit; ++j) {
-        const int32_t slot = mg.first_slot + j;
-        if (j + 1 < mg.nsplit && a.slot_page[slot] >= pages) continue;
-        const float pl = a.part_lse[static_cast<int64_t>(slot) * a.rows_item + i] * kLog2e;
-        if (pl == -INFINITY) continue;
-        const float *po = a.part_o + (static_cast<int64_t>(slot) * a.rows_item + i) * D + lane * E;
-        const float mn = fmaxf(m, pl);
-        const float c0 = m == -INFINITY ? 0.f : exp2f(m - mn), c1 = exp2f(pl - mn);
-        l = l * c0 + c1;
+    for (int32_t j0 = 0; j0 < mg.nsplit; j0 += 32) {
+        const int32_t nj = min(32, mg.nsplit - j0);
+        float w = lane < nj ? pl[static_cast<int64_t>(j0 + lane) * a.rows_item] * kLog2e : -INFINITY;
+        float x[kMergeParts][E];
+        auto load = [&](int32_t j) {
+#pragma unroll
+            for (int k = 0; k < kMergeParts; ++k)
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[k][e] = j + k < nj ? po[(j0 + j + k) * step + e] : 0.f;
+        };
+        load(0);
+        float mx = w;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(FULL, mx, d));
+        const float mn = fmaxf(m, mx);
+        const float base = mn == -INFINITY ? 0.f : mn;
+        const float c0 = exp2f(m - base);  // 0 for m = -inf
+        w = exp2f(w - base);
+        float sum = w;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(FULL, sum, d);
+        l = l * c0 + sum;
         m = mn;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = o[e] * c0 + c1 * po[e];
+        for (int e = 0; e < E; ++e) o[e] *= c0;
+        for (int32_t j = 0; j < nj; j += kMergeParts) {
+            if (j > 0) load(j);
+#pragma unroll
+            for (int k = 0; k < kMergeParts; ++k) {
+                const float wk = __shfl_sync(FULL, w, (j + k) & 31);
+                if (j + k < nj && wk != 0.f) {  // a part of weight 0 may never have been written
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] = fmaf(wk, x[k][e], o[e]);
+                }
+            }
+        }
     }
+    const int32_t r = mg.row0 + i;
+    if (nb < 0 || nb > a.max_draft || tok0 < 0 || static_cast<int64_t>(tok0) + nb > a.n_tokens || r >= nb * a.G) return;
     const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
     const int64_t orow = static_cast<int64_t>(tok0 + r / a.G) * a.Hq + h * a.G + r % a.G;
     uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + orow * D + lane * E);
@@ -744,7 +909,7 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// bf16 tensor map of 1 + `rank` dimensions, boxes of 64 columns, 128-byte swizzle, zeros outside.
+// bf16 tensor map of `rank` dimensions, boxes of 64 columns, 128-byte swizzle, zeros outside.
 int make_map(CUtensorMap *tm, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
              const cuuint32_t *box) {
     EncodeTiledFn fn = encode_fn();
@@ -752,7 +917,7 @@ int make_map(CUtensorMap *tm, const void *base, int rank, const cuuint64_t *dims
         set_cuda_error("cuTensorMapEncodeTiled unavailable", 0);
         return TG_ECUDA;
     }
-    const cuuint32_t one[3] = {1, 1, 1};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
     const CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base),
                           dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -763,11 +928,24 @@ int make_map(CUtensorMap *tm, const void *base, int rank, const cuuint64_t *dims
     return TG_OK;
 }
 
+// A pool of pages as (column of a 64-column half, row of an 8-row group, half, group): one box is a
+// whole page, 4 KB at D = 128, laid out in shared memory group by group, a swizzled atom per half.
 int pool_map(CUtensorMap *tm, const void *base, int32_t D, int64_t pages) {
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(pages) * 16};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * 2};
-    const cuuint32_t box[2] = {64, 16};
-    return make_map(tm, base, 2, dims, strides, box);
+    const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+    const cuuint64_t dims[4] = {64, 8, static_cast<cuuint64_t>(D / 64), static_cast<cuuint64_t>(pages) * 2};
+    const cuuint64_t strides[3] = {row, 128, 8 * row};
+    const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(D / 64), 2};
+    return make_map(tm, base, 4, dims, strides, box);
+}
+
+// Drafted tokens' rows as (column of a half, token, half, head): boxes of 8 tokens of one head, from
+// any token on, in the layout of a page's group.
+int draft_map(CUtensorMap *tm, const void *base, int32_t D, int32_t heads, int64_t n, int64_t stride) {
+    const cuuint64_t row = static_cast<cuuint64_t>(D) * 2;
+    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(D / 64), static_cast<cuuint64_t>(heads)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(stride) * 2, 128, row};
+    const cuuint32_t box[4] = {64, 8, static_cast<cuuint32_t>(D / 64), 1};
+    return make_map(tm, base, 4, dims, strides, box);
 }
 
 // Token rows [n][heads][D] with a token stride (elements): boxes of `hb` heads x `tb` tokens.
@@ -781,41 +959,57 @@ int token_map(CUtensorMap *tm, const void *base, int32_t D, int32_t heads, int64
 
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-constexpr int kItemCost = 8;  // pages' worth of an item's fixed work (draft block, Q, output)
+constexpr int kItemCost = 12;  // pages' worth of an item's fixed work (draft block, Q, output)
+constexpr int kMinShare = 16;  // no worker's share below this many pages' worth
+constexpr int kStaticPermille = 950;
 
-// Work list: every (head, row block) is a run of pages plus a fixed cost; the runs are laid end to
-// end and cut into n_workers equal shares at whole blocks (no share below kMinShare pages).
-constexpr int kMinShare = 16;
-
+// Work list. A unit is a (head, row block): a run of pages plus a fixed cost. Units are taken longest
+// first; the first kStaticPermille of the cost is laid end to end and cut into equal shares, one per
+// worker, at whole blocks. The rest (the shortest heads, mostly whole) become dynamic items that
+// shrink towards the end, none below the size at which writing a part's rows would cost more than an
+// eighth of reading its pages. A small step, which does not fill the machine, is all static.
 void build_items(tg_tree_plan *p, const int32_t *cap, int32_t num_workers) {
     const tg_shape &s = p->shape;
     const int64_t BH = static_cast<int64_t>(s.B) * s.Hkv;
     const int32_t rows = p->max_draft * p->G;
     const int32_t rblocks = (rows + p->rows_item - 1) / p->rows_item;
+    std::vector<int32_t> order(static_cast<size_t>(BH));
+    for (int64_t i = 0; i < BH; ++i) order[static_cast<size_t>(i)] = static_cast<int32_t>(i);
+    std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return cap[x] > cap[y]; });
     int64_t total = 0;
     for (int64_t i = 0; i < BH; ++i) total += (cap[i] + 15) / 16 + kItemCost;
     total *= rblocks;
     const int64_t nw = std::max<int64_t>(1, std::min<int64_t>(num_workers, total / kMinShare));
+    const int64_t fixed = nw == num_workers && nw > 1 && p->tiles == 1 ? total * kStaticPermille / 1000 : total;
+    const int64_t min_dyn = std::max<int64_t>(16, p->rows_item / 4 / kCutPages * kCutPages);
     p->worker_off.assign(1, 0);
     int64_t done = 0;  // cost laid out so far
-    int64_t w = 1;     // the current worker's share ends at total * w / nw
-    for (int64_t i = 0; i < BH; ++i)
+    int64_t w = 1;     // the current worker's share ends at fixed * w / nw
+    for (int32_t i : order)
         for (int32_t rb = 0; rb < rblocks; ++rb) {
             const int32_t pages = (cap[i] + 15) / 16;
             const int32_t first_slot = p->n_slots;
             const size_t first = p->items.size();
             int32_t at = 0;
             for (;;) {
-                while (w < nw && done + kItemCost >= total * w / nw) {  // the share is full
+                int64_t room;  // pages this item may take
+                // the share is full when what is left of it would hold less than a block
+                while (w <= nw && done + (at == 0 ? kItemCost : 0) + kCutPages > fixed * w / nw) {
+                    if (w == nw && fixed == total) break;  // all static: the last worker takes the rest
                     p->worker_off.push_back(static_cast<int32_t>(p->items.size()));
                     ++w;
                 }
-                int64_t room = w < nw ? total * w / nw - done - kItemCost : INT_MAX;
+                if (w <= nw) {
+                    room = w == nw && fixed == total ? INT_MAX : fixed * w / nw - done - (at == 0 ? kItemCost : 0);
+                } else {
+                    room = std::max<int64_t>(min_dyn, (total - done) / (2 * nw));
+                    if (pages - at <= room + room / 2) room = pages - at;
+                }
                 room = std::max<int64_t>(kCutPages, room / kCutPages * kCutPages);
                 int32_t end = static_cast<int32_t>(std::min<int64_t>(pages, at + room));
                 if (pages - end < 2 * kCutPages) end = pages;  // no sliver of a head for the next worker
                 TreeItem it{};
-                it.bh = static_cast<int32_t>(i);
+                it.bh = i;
                 it.page_begin = at;
                 it.page_end = end;
                 it.row0 = rb * p->rows_item;
@@ -829,29 +1023,24 @@ void build_items(tg_tree_plan *p, const int32_t *cap, int32_t num_workers) {
             }
             const int32_t n = static_cast<int32_t>(p->items.size() - first);
             if (n > 1) {
-                for (int32_t j = 0; j < n; ++j) {
-                    p->items[first + j].slot = first_slot + j;
-                    p->slot_page.push_back(p->items[first + j].page_begin);
-                }
+                for (int32_t j = 0; j < n; ++j) p->items[first + j].slot = first_slot + j;
                 p->n_slots += n;
                 TreeMerge mg{};
-                mg.bh = static_cast<int32_t>(i);
+                mg.bh = i;
                 mg.first_slot = first_slot;
                 mg.nsplit = n;
                 mg.row0 = rb * p->rows_item;
-                mg.cap = cap[i];
                 p->merge.push_back(mg);
             }
         }
-    while (static_cast<int64_t>(p->worker_off.size()) < nw) p->worker_off.push_back(static_cast<int32_t>(p->items.size()));
-    p->worker_off.push_back(static_cast<int32_t>(p->items.size()));
-    p->n_workers = static_cast<int32_t>(p->worker_off.size()) - 1;
+    while (static_cast<int64_t>(p->worker_off.size()) <= nw) p->worker_off.push_back(static_cast<int32_t>(p->items.size()));
+    p->n_workers = static_cast<int32_t>(nw);
 }
 
 template <int D, int TILES, bool CAP>
 int set_smem() {
     TG_TRY(cudaFuncSetAttribute(tree_kernel<D, TILES, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                TreeLayout<D, TILES>::kBytes));
+                                TreeLayout<D, TILES>::kLimit));
     return TG_OK;
 }
 template <int D, int TILES>
@@ -889,10 +1078,10 @@ int tree_device_init(tg_tree_plan *p) {
     const int64_t o_items = take(static_cast<int64_t>(p->items.size()) * sizeof(TreeItem));
     const int64_t o_woff = take(static_cast<int64_t>(p->worker_off.size()) * 4);
     const int64_t o_merge = take(static_cast<int64_t>(p->merge.size()) * sizeof(TreeMerge));
-    const int64_t o_spage = take(static_cast<int64_t>(p->slot_page.size()) * 4);
     const int64_t o_lo = take(static_cast<int64_t>(p->row_lo.size()) * 8);
     const int64_t o_hi = take(static_cast<int64_t>(p->row_hi.size()) * 8);
     const int64_t o_err = take(4);
+    const int64_t o_ticket = take(8);
     const int64_t head_bytes = at;
     const int64_t o_po = take(static_cast<int64_t>(p->n_slots) * p->rows_item * p->shape.D * 4);
     const int64_t o_pl = take(static_cast<int64_t>(p->n_slots) * p->rows_item * 4);
@@ -903,7 +1092,6 @@ int tree_device_init(tg_tree_plan *p) {
     put(o_items, p->items.data(), p->items.size() * sizeof(TreeItem));
     put(o_woff, p->worker_off.data(), p->worker_off.size() * 4);
     put(o_merge, p->merge.data(), p->merge.size() * sizeof(TreeMerge));
-    put(o_spage, p->slot_page.data(), p->slot_page.size() * 4);
     put(o_lo, p->row_lo.data(), p->row_lo.size() * 8);
     put(o_hi, p->row_hi.data(), p->row_hi.size() * 8);
     if (cudaMalloc(&p->dev_base, static_cast<size_t>(at)) != cudaSuccess) {
@@ -917,10 +1105,10 @@ int tree_device_init(tg_tree_plan *p) {
     p->d_items = reinterpret_cast<TreeItem *>(d + o_items);
     p->d_worker_off = reinterpret_cast<int32_t *>(d + o_woff);
     p->d_merge = reinterpret_cast<TreeMerge *>(d + o_merge);
-    p->d_slot_page = reinterpret_cast<int32_t *>(d + o_spage);
     p->d_row_lo = reinterpret_cast<int64_t *>(d + o_lo);
     p->d_row_hi = reinterpret_cast<int64_t *>(d + o_hi);
     p->d_err = reinterpret_cast<uint32_t *>(d + o_err);
+    p->d_ticket = reinterpret_cast<uint32_t *>(d + o_ticket);
     p->d_part_o = reinterpret_cast<float *>(d + o_po);
     p->d_part_lse = reinterpret_cast<float *>(d + o_pl);
     return TG_OK;
@@ -938,6 +1126,14 @@ void tree_free(tg_tree_plan *p) {
 struct TreeFree {
     void operator()(tg_tree_plan *p) const { tree_free(p); }
 };
+
+template <int D, int TILES>
+void set_geometry(tg_tree_plan *p) {
+    using TL = TreeLayout<D, TILES>;
+    p->q_boxes = TL::entries(p->q_rows, 2) >= 5 ? 2 : 1;
+    p->entries = TL::entries(p->q_rows, p->q_boxes);
+    p->smem_bytes = TL::q_bytes(p->q_rows, p->q_boxes) + p->entries * TL::kEntry + TL::kControl;
+}
 
 int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft, const int32_t *group_of_head,
                      const int64_t *group_off, int32_t n_groups, int32_t num_workers, int32_t host_only, int32_t device,
@@ -969,6 +1165,12 @@ int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft
     p->tiles = max_draft * G > kRows ? 2 : 1;
     p->rows_item = p->tiles == 2 ? 2 * kRows : max_draft * G;
     p->q_rows = p->tiles == 2 ? kRows : (max_draft * G + 7) / 8 * 8;
+    // a second Q box lets the next item's queries load beside the current one's, where it costs at
+    // most one ring entry
+    if (s->D == 128)
+        p->tiles == 1 ? set_geometry<128, 1>(p.get()) : set_geometry<128, 2>(p.get());
+    else
+        p->tiles == 1 ? set_geometry<64, 1>(p.get()) : set_geometry<64, 2>(p.get());
     p->host_only = host_only != 0;
     if (wait_limit_us > 0) p->wait_ns = static_cast<uint64_t>(wait_limit_us) * 1000ull;
     for (int32_t h = 0; h < s->Hkv; ++h) {
@@ -999,7 +1201,7 @@ int launch_tree(const tg_tree_plan *p, const TreeArgs &a, const CUtensorMap *tm,
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p->n_workers));
     cfg.blockDim = dim3(TL::kThreads);
-    cfg.dynamicSmemBytes = TL::kBytes;
+    cfg.dynamicSmemBytes = static_cast<size_t>(p->smem_bytes);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1099,14 +1301,20 @@ extern "C" int tg_tree_decode(tg_tree_plan *p, int64_t n_tokens, const int32_t *
     int rc = token_map(&tm[0], q, s.D, s.Hq, n_tokens, q_stride, p->G, p->q_rows / p->G);
     if (rc == TG_OK) rc = pool_map(&tm[1], kp, s.D, pool);
     if (rc == TG_OK) rc = pool_map(&tm[2], vp, s.D, pool);
-    if (rc == TG_OK) rc = token_map(&tm[3], k_draft, s.D, s.Hkv, n_tokens, k_stride, 1, 16);
-    if (rc == TG_OK) rc = token_map(&tm[4], v_draft, s.D, s.Hkv, n_tokens, v_stride, 1, 16);
+    if (rc == TG_OK) rc = draft_map(&tm[3], k_draft, s.D, s.Hkv, n_tokens, k_stride);
+    if (rc == TG_OK) rc = draft_map(&tm[4], v_draft, s.D, s.Hkv, n_tokens, v_stride);
     if (rc != TG_OK) return rc;
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     TreeArgs a{};
     a.items = p->d_items;
     a.worker_off = p->d_worker_off;
+    a.n_items = static_cast<int32_t>(p->items.size());
+    a.q_boxes = p->q_boxes;
+    a.entries = p->entries;
+    a.ring = (p->q_boxes * p->tiles * p->q_rows * s.D * 2 + 1023) / 1024 * 1024;
+    a.ticket = p->d_ticket;
     a.G = p->G;
+    a.g_shift = p->G == 1 ? 0 : p->G == 2 ? 1 : p->G == 4 ? 2 : 3;
     a.Hq = s.Hq;
     a.Hkv = s.Hkv;
     a.max_draft = p->max_draft;
@@ -1117,7 +1325,11 @@ extern "C" int tg_tree_decode(tg_tree_plan *p, int64_t n_tokens, const int32_t *
     a.scale_log2 = scale * kLog2e;
     if (softcap > 0.f) {
         a.cap2 = softcap * kLog2e;
-        a.cap_in = 2.f * kLog2e * scale / softcap;
+        a.cap_x_signed = scale / softcap;
+        a.cap_x = std::fabs(a.cap_x_signed);
+        double k = static_cast<double>(scale) / softcap;
+        for (int i = 0; i < 4; ++i, k *= (static_cast<double>(scale) / softcap) * (static_cast<double>(scale) / softcap))
+            a.cap_p[i] = static_cast<float>(static_cast<double>(softcap) * 1.4426950408889634 * kTanh[i] * k);
     }
     a.v_draft = static_cast<const __nv_bfloat16 *>(v_draft);
     a.v_stride = v_stride;
@@ -1138,9 +1350,7 @@ extern "C" int tg_tree_decode(tg_tree_plan *p, int64_t n_tokens, const int32_t *
     if (rc != TG_OK || p->merge.empty()) return rc;
     TreeMergeArgs g{};
     g.merge = p->d_merge;
-    g.slot_page = p->d_slot_page;
     g.draft_off = draft_off;
-    g.kv_len = head_kv_len;
     g.G = p->G;
     g.Hq = s.Hq;
     g.Hkv = s.Hkv;

@@ -179,7 +179,8 @@ def test_plan_covers_every_page_once(seed):
     cap = rng.choice([0, 1, 16, 17, 500, int(rng.integers(1, 9000))], size=B * Hkv)
     info = tg.tg_tree_plan_items(_plan(cap, G * Hkv, Hkv, T, workers=int(rng.choice([0, 1, 7, 400]))))
     it, off = info["items"], info["worker_off"]
-    assert off[0] == 0 and off[-1] == len(it) and np.all(np.diff(off) >= 0) and len(off) == info["n_workers"] + 1
+    # each worker's own items, then those taken by ticket
+    assert off[0] == 0 and off[-1] <= len(it) and np.all(np.diff(off) >= 0) and len(off) == info["n_workers"] + 1
     per = 256 if T * G > 128 else T * G
     rblocks = -(-T * G // per)
     slots = []
@@ -206,6 +207,13 @@ def test_plan_shares_are_even():
     it, off = info["items"], info["worker_off"]
     load = [int((it[a:b, 2] - it[a:b, 1]).sum()) for a, b in zip(off[:-1], off[1:])]
     assert info["n_workers"] == 296 and max(load) <= 1.12 * np.mean(load)
+    dyn = it[off[-1]:]
+    left = (dyn[:, 2] - dyn[:, 1]).sum() / (it[:, 2] - it[:, 1]).sum()
+    assert 0.02 < left < 0.1                              # the rest is taken by ticket
+    size = dyn[:, 2] - dyn[:, 1]
+    assert size.max() <= 64                               # in small items
+    small = tg.tg_tree_plan_items(_plan([500] * 8, 8, 8, 4))
+    assert small["worker_off"][-1] == small["n_items"]    # a small step is all static
 
 
 @pytest.mark.parametrize("kw,status", [
