@@ -83,10 +83,11 @@ __device__ __forceinline__ int64_t kept_rows(const CompactArgs &a, int32_t bh) {
     return b < 0 || e < b || e > a.n_keep || e - b > max(0, a.budget[bh]) ? -1 : e - b;
 }
 
-// One warp per 32 entries of the keep list, whatever heads they belong to, so heads of very
+// One warp per TPW entries of the keep list, whatever heads they belong to, so heads of very
 // different budgets cost the same per row. Lane l finds entry l's head (binary search of
 // keep_off, the same few cached words for every lane), its source and destination rows; then the
-// warp copies the 32 K rows and 32 V rows 16 bytes a lane, the rows' addresses by shuffle.
+// warp copies the K rows and the V rows 16 bytes a lane, the rows' addresses by shuffle.
+template <int TPW>
 __global__ void __launch_bounds__(kCompactWarps * 32) compact_kernel(const __grid_constant__ CompactArgs a) {
     constexpr unsigned FULL = 0xffffffffu;
     const int lane = threadIdx.x & 31;
@@ -97,9 +98,9 @@ __global__ void __launch_bounds__(kCompactWarps * 32) compact_kernel(const __gri
         a.kv_len[gtid] = m < 0 ? 0 : static_cast<int32_t>(m);
         if (m < 0) atomicAdd(a.n_bad, 1);
     }
-    const int64_t i = (gtid >> 5) * 32 + lane;  // keep-list entry of this lane
+    const int64_t i = (gtid >> 5) * TPW + lane;  // keep-list entry of this lane
     int64_t src = -1, dst = -1;
-    if (i < a.n_keep) {
+    if (lane < TPW && i < a.n_keep) {
         int32_t lo = 0, hi = a.BH;  // the last head whose list starts at or before i
         while (hi - lo > 1) {
             const int32_t mid = (lo + hi) >> 1;
@@ -122,8 +123,8 @@ __global__ void __launch_bounds__(kCompactWarps * 32) compact_kernel(const __gri
         }
     }
     if (!__any_sync(FULL, src >= 0)) return;
-    // vector v of the warp's 32 rows: row v / row_vec, K first, then V
-    const int per = 32 * a.row_vec;
+    // vector v of the warp's rows: row v / row_vec, K first, then V
+    const int per = TPW * a.row_vec;
     for (int v0 = 0; v0 < 2 * per; v0 += 32 * kCopyVec) {
         uint4 x[kCopyVec];
         uint4 *to[kCopyVec];
@@ -234,7 +235,11 @@ extern "C" int tg_compact_kv(const tg_shape *s, int64_t src_num_pages, const voi
     a.keep = keep_idx;
     a.kv_len = head_kv_len;
     a.n_bad = n_bad;
-    const int64_t threads = n_keep > BH ? n_keep : BH;
-    return launch(compact_kernel, a, (threads + kCompactWarps * 32 - 1) / (kCompactWarps * 32), kCompactWarps * 32,
-                  stream, "compact_kernel");
+    // 32 entries a warp (1.3 M kept rows of D = 128: 220 us, 6.1 TB/s, against 272 us with 8); lists too
+    // short to give every SM 16 such warps go 8 entries a warp (17 000 rows: 5.3 us against 9.5 us)
+    const bool few = n_keep < 148 * 16 * 32;
+    const int64_t threads = few ? (n_keep + 7) / 8 * 32 : n_keep;
+    const int64_t most = threads > BH ? threads : BH;
+    return launch(few ? compact_kernel<8> : compact_kernel<32>, a,
+                  (most + kCompactWarps * 32 - 1) / (kCompactWarps * 32), kCompactWarps * 32, stream, "compact_kernel");
 }

@@ -19,9 +19,9 @@
 namespace tg {
 namespace {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeRows = 3;    // head rows of a lane group in flight
-constexpr int kRopeMaxD = 256;  // a head row is at most one warp of 16-byte slices
+constexpr int kRopeThreads = 128;
+constexpr int kRopeRows = 5;    // head rows of a lane group in flight
+constexpr int kRopeMaxD = 256;  // a head row is at most one warp of 8-element lanes
 
 struct RopeArgs {
     const __nv_bfloat16 *x[2];   // q, k
@@ -30,7 +30,7 @@ struct RopeArgs {
     int64_t in_stride[2], out_stride[2];
     int32_t heads[2];
     int32_t D, rot;
-    float eps, rot_scale;
+    float inv_d, eps, rot_scale;
     const int32_t *pos;
     const double *inv_freq;
 };
@@ -38,41 +38,82 @@ struct RopeArgs {
 __device__ __forceinline__ float lo16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi16(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 
-__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[8]) {
-    f[0] = lo16(v.x); f[1] = hi16(v.x); f[2] = lo16(v.y); f[3] = hi16(v.y);
-    f[4] = lo16(v.z); f[5] = hi16(v.z); f[6] = lo16(v.w); f[7] = hi16(v.w);
+// A lane's 8 elements of a head row as four pairs (a_i, b_i) that turn together: A = a_0..3, B = b_0..3.
+// Interleaved: words hold (a_i, b_i). Halves: the first two words hold a_0..3, the last two b_0..3.
+template <bool INTER>
+__device__ __forceinline__ void unpack(const uint4 &v, ptx::f2 (&A)[2], ptx::f2 (&B)[2]) {
+    if (INTER) {
+        A[0] = ptx::pair(lo16(v.x), lo16(v.y));
+        A[1] = ptx::pair(lo16(v.z), lo16(v.w));
+        B[0] = ptx::pair(hi16(v.x), hi16(v.y));
+        B[1] = ptx::pair(hi16(v.z), hi16(v.w));
+    } else {
+        A[0] = ptx::pair(lo16(v.x), hi16(v.x));
+        A[1] = ptx::pair(lo16(v.y), hi16(v.y));
+        B[0] = ptx::pair(lo16(v.z), hi16(v.z));
+        B[1] = ptx::pair(lo16(v.w), hi16(v.w));
+    }
 }
 
-// One CTA per token. A head row of D bf16 is D/8 16-byte slices, one per lane of a group of LPH
-// lanes (LPH = D/8 rounded up to a power of two), so a row is read and written once, a norm is a
-// few xor-shuffles, and the partner of a half-layout pair sits rot/16 lanes away (rot % 16 == 0).
+template <bool INTER>
+__device__ __forceinline__ uint4 repack(const ptx::f2 (&A)[2], const ptx::f2 (&B)[2]) {
+    float a[4], b[4];
+    ptx::split(A[0], a[0], a[1]);
+    ptx::split(A[1], a[2], a[3]);
+    ptx::split(B[0], b[0], b[1]);
+    ptx::split(B[1], b[2], b[3]);
+    if (INTER)
+        return make_uint4(ptx::pack_bf16(a[0], b[0]), ptx::pack_bf16(a[1], b[1]), ptx::pack_bf16(a[2], b[2]), ptx::pack_bf16(a[3], b[3]));
+    return make_uint4(ptx::pack_bf16(a[0], a[1]), ptx::pack_bf16(a[2], a[3]), ptx::pack_bf16(b[0], b[1]), ptx::pack_bf16(b[2], b[3]));
+}
+
+// One CTA per token. A head row of D bf16 takes D/8 lanes of a group of LPH (D/8 rounded up to a power
+// of two): 16 bytes a lane, or for halves 8 bytes from each half of the rotated part, so that both
+// elements of a pair are in one lane and rotating needs no shuffle; a row is read and written once.
 // The token's angles are the same for all heads: rot/2 of them in 64 bits (position * frequency
 // in turns, reduced to one turn before it is rounded to 32 bits: a position of 10^6 keeps its
 // angle to 2^-24 of a turn), their sines and cosines once in shared memory while the rows' loads
-// are in flight. Norm, weight and rotation stay in fp32; the only rounding is the output's.
-// Bound: DRAM (4 D bytes per head row).
+// are in flight. Norm, weight and rotation stay in fp32, two elements an instruction; the only
+// rounding is the output's. Bound: DRAM (4 D bytes per head row): 32001 tokens of 32 + 8 heads of
+// D = 128 take 120 us, 5.46 TB/s. 8 CTAs per SM of 5 rows a lane measured best (3 rows of 256 threads
+// 145 us, 10 CTAs at fewer registers 128 us, 64 threads 122 us).
 template <int LPH, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 8) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
+    using ptx::f2;
     __shared__ float2 cs[kRopeMaxD / 2];
     constexpr int GROUPS = kRopeThreads / LPH;  // head rows per pass
     const int64_t n = blockIdx.x;
     const int sub = threadIdx.x % LPH, grp = threadIdx.x / LPH;
+    const int warp_grp = (threadIdx.x & ~31) / LPH;  // the warp's first group
     const int H = a.heads[0] + a.heads[1];
-    const int nvec = a.D / 8;
+    const bool on = sub < a.D / 8;
     const int half = a.rot / 2;
+    // element offsets of the lane's two 8-byte parts
+    const int turning = a.rot / 8;  // lanes that hold pairs of halves
+    const int e0 = INTER || sub >= turning ? 8 * sub : 4 * sub;
+    const int e1 = INTER || sub >= turning ? 8 * sub + 4 : half + 4 * sub;
     ptx::grid_wait();
     ptx::grid_launch();
 
-    auto row_in = [&](int hd) {
-        const int s = hd >= a.heads[0];
-        return reinterpret_cast<const uint4 *>(a.x[s] + n * a.in_stride[s] + static_cast<int64_t>(hd - s * a.heads[0]) * a.D);
+    auto load = [&](const __nv_bfloat16 *row) {
+        if (INTER) return *reinterpret_cast<const uint4 *>(row + e0);
+        const uint2 u = *reinterpret_cast<const uint2 *>(row + e0), w = *reinterpret_cast<const uint2 *>(row + e1);
+        return make_uint4(u.x, u.y, w.x, w.y);
     };
+    auto offset = [&](int hd, const int64_t (&stride)[2]) {
+        const int s = hd >= a.heads[0];
+        return n * stride[s] + static_cast<int64_t>(hd - (s ? a.heads[0] : 0)) * a.D;
+    };
+    const f2 one = ptx::pair(1.f, 1.f);
+    f2 C[2] = {one, one}, S[2], NS[2];
+    bool turn[4] = {false, false, false, false};
     for (int h0 = 0; h0 < H; h0 += GROUPS * kRopeRows) {
         uint4 v[kRopeRows];
 #pragma unroll
         for (int j = 0; j < kRopeRows; ++j) {
             const int hd = h0 + j * GROUPS + grp;
-            v[j] = hd < H && sub < nvec ? row_in(hd)[sub] : make_uint4(0u, 0u, 0u, 0u);
+            v[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (hd < H && on) v[j] = load(a.x[hd >= a.heads[0]] + offset(hd, a.in_stride));
         }
         if (h0 == 0) {
             for (int i = threadIdx.x; i < half; i += kRopeThreads) {
@@ -83,62 +124,82 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const __grid_co
                 cs[i] = make_float2(c * a.rot_scale, s * a.rot_scale);
             }
             __syncthreads();
+            float c[4], s[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                turn[i] = 4 * sub + i < half;
+                const float2 t = turn[i] ? cs[4 * sub + i] : make_float2(1.f, 0.f);
+                c[i] = t.x;
+                s[i] = t.y;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                C[k] = ptx::pair(c[2 * k], c[2 * k + 1]);
+                S[k] = ptx::pair(s[2 * k], s[2 * k + 1]);
+                NS[k] = ptx::pair(-s[2 * k], -s[2 * k + 1]);
+            }
         }
 #pragma unroll
         for (int j = 0; j < kRopeRows; ++j) {
+            if (h0 + j * GROUPS + warp_grp >= H) break;  // no row of this warp
             const int hd = h0 + j * GROUPS + grp;
-            const int s = hd >= a.heads[0];
-            float x[8];
-            unpack(v[j], x);
-            float r = 1.f;
-            const __nv_bfloat16 *w = a.w[s];
-            float ss = 0.f;
+            const int side = hd >= a.heads[0];
+            f2 A[2], B[2];
+            unpack<INTER>(v[j], A, B);
+            const __nv_bfloat16 *w = a.w[side];
+            if (a.w[0] || a.w[1]) {
+                const f2 q = ptx::add2(ptx::fma2(A[0], A[0], ptx::mul2(A[1], A[1])), ptx::fma2(B[0], B[0], ptx::mul2(B[1], B[1])));
+                float s0, s1;
+                ptx::split(q, s0, s1);
+                float ss = s0 + s1;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+                for (int d = LPH / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+                if (w && on) {
+                    const float r = rsqrtf(fmaf(ss, a.inv_d, a.eps));
+                    f2 WA[2], WB[2];
+                    unpack<INTER>(load(w), WA, WB);
+                    const f2 rr = ptx::pair(r, r);
 #pragma unroll
-            for (int d = LPH / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-            if (w) r = rsqrtf(ss / static_cast<float>(a.D) + a.eps);
-            const uint4 one = make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
-            float wf[8];
-            unpack(w && sub < nvec ? __ldg(reinterpret_cast<const uint4 *>(w) + sub) : one, wf);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= r * wf[e];
-            if (INTER) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int i = 4 * sub + e;
-                    if (i < half) {
-                        const float2 t = cs[i];
-                        const float x0 = x[2 * e], x1 = x[2 * e + 1];
-                        x[2 * e] = x0 * t.x - x1 * t.y;
-                        x[2 * e + 1] = x0 * t.y + x1 * t.x;
-                    }
-                }
-            } else {
-                // the partner slice sits half / 8 lanes up (first half) or down (second half)
-                const int step = half / 8;
-                const bool first = sub < step, turned = sub < 2 * step;
-                const int other = !turned ? sub : (first ? sub + step : sub - step);
-                const float sign = first ? -1.f : 1.f;
-                float p[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, x[e], other, LPH);
-                if (turned) {
-                    const int i = 8 * (first ? sub : sub - step);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float2 t = cs[i + e];
-                        x[e] = x[e] * t.x + sign * p[e] * t.y;
+                    for (int k = 0; k < 2; ++k) {
+                        A[k] = ptx::mul2(ptx::mul2(A[k], rr), WA[k]);
+                        B[k] = ptx::mul2(ptx::mul2(B[k], rr), WB[k]);
                     }
                 }
             }
-            if (hd < H && sub < nvec) {
-                uint4 o;
-                o.x = ptx::pack_bf16(x[0], x[1]);
-                o.y = ptx::pack_bf16(x[2], x[3]);
-                o.z = ptx::pack_bf16(x[4], x[5]);
-                o.w = ptx::pack_bf16(x[6], x[7]);
-                reinterpret_cast<uint4 *>(a.y[s] + n * a.out_stride[s] + static_cast<int64_t>(hd - s * a.heads[0]) * a.D)[sub] = o;
+            if (turn[0]) {
+                f2 U[2], V[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    U[k] = ptx::fma2(B[k], NS[k], ptx::mul2(A[k], C[k]));
+                    V[k] = ptx::fma2(A[k], S[k], ptx::mul2(B[k], C[k]));
+                }
+                if (turn[3]) {
+                    A[0] = U[0]; A[1] = U[1]; B[0] = V[0]; B[1] = V[1];
+                } else {  // the rotated part ends inside this lane
+                    float a0[4], b0[4], u[4], w0[4];
+                    ptx::split(A[0], a0[0], a0[1]); ptx::split(A[1], a0[2], a0[3]);
+                    ptx::split(B[0], b0[0], b0[1]); ptx::split(B[1], b0[2], b0[3]);
+                    ptx::split(U[0], u[0], u[1]); ptx::split(U[1], u[2], u[3]);
+                    ptx::split(V[0], w0[0], w0[1]); ptx::split(V[1], w0[2], w0[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (turn[i]) {
+                            a0[i] = u[i];
+                            b0[i] = w0[i];
+                        }
+                    A[0] = ptx::pair(a0[0], a0[1]); A[1] = ptx::pair(a0[2], a0[3]);
+                    B[0] = ptx::pair(b0[0], b0[1]); B[1] = ptx::pair(b0[2], b0[3]);
+                }
+            }
+            if (hd < H && on) {
+                __nv_bfloat16 *row = a.y[side] + offset(hd, a.out_stride);
+                const uint4 o = repack<INTER>(A, B);
+                if (INTER) {
+                    *reinterpret_cast<uint4 *>(row + e0) = o;
+                } else {
+                    *reinterpret_cast<uint2 *>(row + e0) = make_uint2(o.x, o.y);
+                    *reinterpret_cast<uint2 *>(row + e1) = make_uint2(o.z, o.w);
+                }
             }
         }
     }
@@ -231,6 +292,7 @@ extern "C" int tg_qk_norm_rope(int64_t n_tokens, int32_t Hq, int32_t Hkv, int32_
     }
     a.D = D;
     a.rot = rot_dim;
+    a.inv_d = 1.f / static_cast<float>(D);
     a.eps = eps;
     a.rot_scale = rot_scale;
     a.pos = position;

@@ -312,9 +312,10 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
 }
 
 // Path append (sink + recent rule, several tokens): the accepted drafted tokens of a sequence,
-// appended in order as append_kernel<0> would one by one. WPH warps per (b, h), a token per warp
-// round: every lane holds two tokens of the path (at most 64), so all slots and page ids of a head
-// are found in one round of loads, and the rows of kPathRound tokens are in flight together.
+// appended in order as append_kernel<0> would one by one. WPH warps per (b, h): every lane holds two
+// tokens of the path (at most 64), so all slots and page ids of a head are found in one round of
+// loads; then the warps copy the tokens' K and V rows as one run of 16-byte vectors, kPathRound of a
+// lane in flight.
 //   Token i of m (length n, budget R + s, s sinks, cursor c): the free slot n + i while
 //   n + i < budget, else ring slot s + (c + o) mod R with o = n + i - budget. A later token of the
 //   path replaces it when o + R is still in the path, or, for a free slot s + x, when the ring comes
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
 // pool, is left as it was. Bound: launch and load latency (offsets, page id, row); moves 8 D bytes
 // per accepted token and head.
 constexpr int kPathMax = 64;   // accepted tokens of one sequence at most
-constexpr int kPathRound = 4;  // tokens of a warp in flight
+constexpr int kPathRound = 4;  // 16-byte vectors of a lane in flight
 template <int WPH>
 __global__ void __launch_bounds__(kAppendWarps * 32)
     append_path_kernel(int32_t BH, int32_t Hkv, int32_t D, int64_t num_pages, int32_t sink, int64_t n_draft,
@@ -385,29 +386,30 @@ __global__ void __launch_bounds__(kAppendWarps * 32)
     const int nvec = D / 8;
     if (on && !bad) {
         const int32_t h = bh % Hkv;
-        for (int i0 = part * kPathRound; i0 < m; i0 += WPH * kPathRound) {
-            for (int v0 = 0; v0 < 2 * nvec; v0 += 32) {
-                const int v = v0 + lane;
-                uint4 x[kPathRound];
-                uint4 *to[kPathRound];
+        const int total = m * 2 * nvec;  // vectors of the path's rows: token, K then V, vector
+        for (int v0 = part * 32 * kPathRound; v0 < total; v0 += WPH * 32 * kPathRound) {
+            uint4 x[kPathRound];
+            uint4 *to[kPathRound];
 #pragma unroll
-                for (int r = 0; r < kPathRound; ++r) {
-                    const int i = i0 + r;
-                    const int64_t tk = __shfl_sync(FULL, i < 32 ? tok[0] : tok[1], i & 31);
-                    const int64_t rw = __shfl_sync(FULL, i < 32 ? row[0] : row[1], i & 31);
-                    const bool lv = __shfl_sync(FULL, static_cast<int>(i < 32 ? live[0] : live[1]), i & 31) != 0;
-                    to[r] = nullptr;
-                    if (i < m && lv && v < 2 * nvec) {
-                        const bool is_v = v >= nvec;
-                        const int u = is_v ? v - nvec : v;
-                        x[r] = (is_v ? v_draft + tk * v_stride : k_draft + tk * k_stride)[h * nvec + u];
-                        to[r] = (is_v ? v_pages : k_pages) + rw * nvec + u;
-                    }
+            for (int r = 0; r < kPathRound; ++r) {
+                const int v = v0 + 32 * r + lane;
+                const int i = v < total ? v / (2 * nvec) : 0;
+                const int u = v - i * 2 * nvec;
+                const int64_t t_lo = __shfl_sync(FULL, tok[0], i & 31), t_hi = __shfl_sync(FULL, tok[1], i & 31);
+                const int64_t r_lo = __shfl_sync(FULL, row[0], i & 31), r_hi = __shfl_sync(FULL, row[1], i & 31);
+                const int alive = __shfl_sync(FULL, (live[0] ? 1 : 0) | (live[1] ? 2 : 0), i & 31);
+                const int64_t tk = i < 32 ? t_lo : t_hi, rw = i < 32 ? r_lo : r_hi;
+                to[r] = nullptr;
+                if (v < total && (alive >> (i >> 5) & 1)) {
+                    const bool is_v = u >= nvec;
+                    const int w = is_v ? u - nvec : u;
+                    x[r] = (is_v ? v_draft + tk * v_stride : k_draft + tk * k_stride)[h * nvec + w];
+                    to[r] = (is_v ? v_pages : k_pages) + rw * nvec + w;
                 }
-#pragma unroll
-                for (int r = 0; r < kPathRound; ++r)
-                    if (to[r]) *to[r] = x[r];
             }
+#pragma unroll
+            for (int r = 0; r < kPathRound; ++r)
+                if (to[r]) *to[r] = x[r];
         }
     }
     __syncthreads();
@@ -496,8 +498,13 @@ extern "C" int tg_append_path_sink_recent(const tg_shape *shape, int32_t sink, i
     if (n_draft > 0 && (!k_draft || !v_draft || k_stride < width || v_stride < width || k_stride % 8 != 0 ||
                         v_stride % 8 != 0))
         return TG_EINVAL;
-    // one warp per head copies kPathRound tokens a round; longer paths get more warps per head
-    const int wph = max_path <= kPathRound ? 1 : max_path <= 2 * kPathRound ? 2 : max_path <= 4 * kPathRound ? 4 : 8;
+    // A warp per head while the heads alone fill the machine (4096 heads of D = 64, paths of up
+    // to 29 tokens: 11.7 us with 1 warp a head, 12.3 with 2, 16.0 with 4, 21.6 with 8); fewer heads
+    // get up to 8 warps each, as many as the longest path has rounds of vectors (512 heads of
+    // D = 128, up to 6 tokens: 4.3 us with 1, 3.5 with 2, 3.7 with 4).
+    const int64_t rounds = (static_cast<int64_t>(max_path) * 2 * (shape->D / 8) + 32 * kPathRound - 1) / (32 * kPathRound);
+    int wph = 1;
+    while (wph < 8 && wph < rounds && static_cast<int64_t>(BH) * wph < 148 * 16) wph *= 2;
     auto kern = wph == 1 ? append_path_kernel<1> : wph == 2 ? append_path_kernel<2>
               : wph == 4 ? append_path_kernel<4> : append_path_kernel<8>;
     const int heads = kAppendWarps / wph;
