@@ -133,7 +133,7 @@ _SIGS = [
     ("tg_tree_plan_create", ctypes.c_int, [ctypes.POINTER(tg_shape), _P, _I32, _P, _P, _I32, _I32,
                                            _I32, _I32, _I32, ctypes.POINTER(_P)]),
     ("tg_tree_plan_destroy", None, [_P]),
-    ("tg_tree_plan_items", ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P]),
+    ("tg_tree_plan_items", ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, _P]),
     ("tg_tree_plan_status", ctypes.c_int, [_P, _P]),
     ("tg_tree_decode", ctypes.c_int, [_P, _I64, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P,
                                       _P, _F32, _F32, _P, _P, _P]),
@@ -980,13 +980,14 @@ def tg_tree_plan_destroy(plan: TreePlan):
 
 def tg_tree_plan_items(plan: TreePlan) -> dict:
     """Counts, items int32[n, 8] and worker_off int32[n_workers + 1] (see include/tg.h)."""
-    n, w, m, nbytes = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int64()
-    refs = [ctypes.byref(x) for x in (n, w, m, nbytes)]
+    n, w, m, rows, nbytes = (ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32(),
+                             ctypes.c_int64())
+    refs = [ctypes.byref(x) for x in (n, w, m, rows, nbytes)]
     _check(_lib().tg_tree_plan_items(plan.handle, *refs, None, None), "tg_tree_plan_items")
     items = np.empty((n.value, 8), dtype=np.int32)
     off = np.empty(w.value + 1, dtype=np.int32)
     _check(_lib().tg_tree_plan_items(plan.handle, *refs, _hp(items), _hp(off)), "tg_tree_plan_items")
-    return dict(n_items=n.value, n_workers=w.value, n_merge=m.value, device_bytes=nbytes.value,
+    return dict(n_items=n.value, n_workers=w.value, n_merge=m.value, rows=rows.value, device_bytes=nbytes.value,
                 items=items, worker_off=off)
 
 

@@ -94,6 +94,23 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
         : TG_R8(r, 0), TG_R8(r, 8), TG_R8(r, 16), TG_R8(r, 24), TG_R8(r, 32), TG_R8(r, 40), TG_R8(r, 48), TG_R8(r, 56)
         : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];" : TG_R8(r, 0) : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : TG_R8(r, 0), TG_R8(r, 8)
+        : "r"(taddr));
+}
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+    static_assert(N == 8 || N == 16 || N == 32 || N == 64, "columns");
+    if constexpr (N == 8) tmem_ld8(taddr, r);
+    else if constexpr (N == 16) tmem_ld16(taddr, r);
+    else if constexpr (N == 32) tmem_ld32(taddr, r);
+    else tmem_ld64(taddr, r);
+}
 // 16 lanes x 64 columns: thread t holds of column pair 8 k + 2 (t % 4) row t / 4 in r[4 k], r[4 k + 1] and
 // row t / 4 + 8 in r[4 k + 2], r[4 k + 3].
 __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {
@@ -109,6 +126,9 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
         ::"r"(taddr), TG_W8(r, 0), TG_W8(r, 8), TG_W8(r, 16), TG_W8(r, 24)
         : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), TG_W8(r, 0) : "memory");
 }
 #undef TG_R8
 #undef TG_W8

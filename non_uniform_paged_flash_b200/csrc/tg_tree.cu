@@ -55,6 +55,7 @@ struct tg_tree_plan {
     int32_t n_workers = 0;
     int32_t rows_item = 0;   // query rows of an item at most
     int32_t q_rows = 0;      // rows of one Q box (multiple of 8)
+    int32_t narrow = 0;      // rows of the narrow kernel (16 or 32), 0: wide kernel
     int32_t q_boxes = 1;     // Q boxes in shared memory
     int32_t entries = 0;     // K / V ring entries
     int32_t smem_bytes = 0;
@@ -87,6 +88,9 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 // Block header flags.
 constexpr int32_t kFirst = 1, kLast = 2, kDraft = 4, kStop = 8;
+// The narrow kernel's, whose kFirst and kLast are per stream: the item's own ends, and whether it takes
+// the drafted tokens.
+constexpr int32_t kOpen = 16, kClose = 32, kTakesDraft = 64;
 
 // What the block's consumers need to know, written by the producer before the block's K arrives.
 struct alignas(16) BlockHdr {
@@ -155,6 +159,159 @@ __device__ __forceinline__ bool any_nonfinite(uint32_t w) {  // two bf16: an exp
     return (((w & 0x7F807F80u) + 0x00800080u) & 0x80008000u) != 0u;
 }
 
+// A CTA's way through its items, for the producer warp: its own list, then dynamic items by ticket.
+struct ItemWalk {
+    const TreeArgs &a;
+    int32_t i1, n_static;
+    const int lane;
+    int32_t cur;   // current item, -1 at the end
+    ItemState nx;  // its state
+
+    __device__ __forceinline__ ItemWalk(const TreeArgs &args, int32_t i0, int32_t end, int32_t stat, const TreeItem &first, int l)
+        : a(args), i1(end), n_static(stat), lane(l), nx{} {
+        cur = i0 < i1 ? i0 : after(i1 - 1);
+        if (cur >= 0) nx = state_of(i0 < end ? first : a.items[cur]);
+    }
+    __device__ __forceinline__ ItemState state_of(const TreeItem &it) const {
+        ItemState s;
+        s.it = it;
+        const int32_t b = it.bh / a.Hkv;
+        s.tok0 = a.draft_off[b];
+        s.nb = a.draft_off[b + 1] - s.tok0;
+        s.len = a.kv_len[it.bh];
+        s.off = a.head_off[it.bh];
+        return s;
+    }
+    __device__ __forceinline__ int32_t after(int32_t i) {
+        if (i + 1 < i1) return i + 1;
+        if (n_static >= a.n_items) return -1;
+        int32_t k = 0;
+        if (lane == 0) k = static_cast<int32_t>(atomicAdd(a.ticket, 1u));
+        k = n_static + __shfl_sync(0xffffffffu, k, 0);
+        if (k >= a.n_items) return -1;
+        i1 = 0;  // from here on by ticket
+        return k;
+    }
+    __device__ __forceinline__ bool own_next() const { return cur + 1 < i1; }
+    __device__ __forceinline__ void advance() {
+        cur = after(cur);
+        if (cur >= 0) nx = state_of(a.items[cur]);
+    }
+    // one lane, once: the last CTA to come here readies the tickets for the next call
+    __device__ __forceinline__ void finish() const {
+        if (n_static < a.n_items && atomicAdd(a.ticket + 1, 1u) == gridDim.x - 1) {
+            a.ticket[0] = 0u;
+            a.ticket[1] = 0u;
+        }
+    }
+};
+
+// What an item amounts to under the current lengths.
+struct ItemShape {
+    int32_t h, nrow, np, nc;  // KV head, query rows, pages that hold tokens, blocks of them
+
+    // False: nothing to do. A bad sequence or head is reported and skipped whole: nothing of it is
+    // read. A part of a growing head that holds nothing yet is marked empty for the merge.
+    __device__ __forceinline__ bool of(const TreeArgs &a, const ItemState &s, int block_pages, int lane) {
+        const int32_t b = s.it.bh / a.Hkv;
+        h = s.it.bh - b * a.Hkv;
+        uint32_t err = 0;
+        if (s.nb < 0 || s.nb > a.max_draft || s.tok0 < 0 || static_cast<int64_t>(s.tok0) + s.nb > a.n_tokens) err |= kErrPlan;
+        if (s.len < 0 || s.len > s.it.cap) err |= kErrPlan;
+        const int32_t pages = (s.len + 15) / 16;
+        if (!err && pages > 0 && (s.off < a.row_lo[h] || s.off + pages > a.row_hi[h])) err |= kErrBadRow;
+        if (err) {
+            if (lane == 0) atomicOr(a.err, err);
+            return false;
+        }
+        nrow = min(s.nb * a.G - s.it.row0, a.rows_item);
+        if (nrow <= 0) return false;
+        np = max(0, min(s.it.page_end, pages) - s.it.page_begin);
+        nc = (np + block_pages - 1) / block_pages;
+        if (nc + s.it.draft == 0) {
+            for (int32_t r = lane; r < nrow; r += 32) a.part_lse[static_cast<int64_t>(s.it.slot) * a.rows_item + r] = -INFINITY;
+            return false;
+        }
+        return true;
+    }
+};
+
+// One warp: zeros the V rows between the nv valid tokens and the end of their 16-row box (stale rows
+// may hold NaN, which a zero probability does not silence); of drafted V rows, zeros infinities and
+// NaN and marks their tokens in *bad (their elements are added back for the rows that see them).
+template <int HALVES>
+__device__ __forceinline__ void clean_v(uint32_t v, int32_t nv, bool draft, unsigned long long *bad, int lane) {
+    constexpr int CH = 8 * HALVES;  // 16-byte chunks of a row
+    const int32_t end = (nv + 15) & ~15;
+    auto at = [&](int32_t r, int32_t q) { return v + (r >> 3) * (1024 * HALVES) + (q >> 3) * 1024 + (r & 7) * 128 + (((q & 7) ^ (r & 7)) << 4); };
+    for (int32_t c = lane; c < (end - nv) * CH; c += 32)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at(nv + c / CH, c % CH)), "r"(0u) : "memory");
+    if (draft) {
+        for (int32_t r = lane; r < nv; r += 32) {
+            uint32_t seen = 0u;
+#pragma unroll
+            for (int q = 0; q < CH; ++q) {
+                uint4 x;
+                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at(r, q)) : "memory");
+                if (any_nonfinite(x.x) | any_nonfinite(x.y) | any_nonfinite(x.z) | any_nonfinite(x.w)) seen |= 1u << q;
+            }
+            if (seen) {
+                atomicOr(bad, 1ull << r);
+                __threadfence_block();
+                for (int q = 0; q < CH; ++q)
+                    if (seen >> q & 1u)
+                        for (int w = 0; w < 8; ++w) {
+                            uint16_t x;
+                            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at(r, q) + 2 * w) : "memory");
+                            if ((x & 0x7F80u) == 0x7F80u)
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(at(r, q) + 2 * w), "h"(static_cast<uint16_t>(0)) : "memory");
+                        }
+            }
+        }
+    }
+    ptx::fence_async_smem();
+    __syncwarp();
+}
+
+// tanh on |x| <= kTanhNear as x p(x^2), p of degree 3 fitted for the least maximum relative error
+// (Lawson's reweighted least squares; 9.8e-08 in exact arithmetic). Scores of a capped head are mostly
+// this small, and five multiplications and additions on pairs of scores cost less than the general
+// form's two special-function calls each (three with the exponential, on a quarter-rate unit that
+// bounds wide drafts). The host folds the scales into the coefficients.
+constexpr float kTanhNear = 0.4f;
+constexpr double kTanh[4] = {0.999999901901, -0.333313624587, 0.132709767556, -0.0475536034831};
+
+// Capped scores in log2 units, in place: c tanh(s scale / c) log2 e.
+template <int N>
+__device__ __forceinline__ void cap_scores(uint32_t (&sr)[N], const TreeArgs &a) {
+    using namespace ptx;
+    float far = 0.f;
+#pragma unroll
+    for (int c = 0; c < N; c += 2) far = max3(far, fabsf(__uint_as_float(sr[c])), fabsf(__uint_as_float(sr[c + 1])));
+    if (__all_sync(0xffffffffu, far * a.cap_x <= kTanhNear)) {
+        const f2 c0 = pair(a.cap_p[0], a.cap_p[0]), c1 = pair(a.cap_p[1], a.cap_p[1]), c2 = pair(a.cap_p[2], a.cap_p[2]),
+                 c3 = pair(a.cap_p[3], a.cap_p[3]);
+#pragma unroll
+        for (int c = 0; c < N; c += 2) {
+            const f2 x = pair(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+            const f2 y = mul2(x, x);
+            const f2 p = mul2(x, fma2(fma2(fma2(c3, y, c2), y, c1), y, c0));
+            float u, w;
+            split(p, u, w);
+            sr[c] = __float_as_uint(u);
+            sr[c + 1] = __float_as_uint(w);
+        }
+    } else {
+        // tanh(x) = 1 - 2 / (1 + e^2x): absolute error of a few 2^-24 c, limits +-c
+        const float k2 = 2.f * kLog2e * a.cap_x_signed;
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+            const float e = ex2(__uint_as_float(sr[c]) * k2);
+            sr[c] = __float_as_uint(a.cap2 * fmaf(-2.f, rcp(1.f + e), 1.f));
+        }
+    }
+}
+
 // ------------------------------------------------------------------------------------------
 // Tree kernel: a persistent CTA per worker walks the worker's items (equal shares of most of the
 // reserved pages, cut ahead of time), then items of the rest by ticket, which evens out what the
@@ -178,14 +335,6 @@ __device__ __forceinline__ bool any_nonfinite(uint32_t w) {  // two bf16: an exp
 // tokens are zeroed in shared memory before the product (0 * NaN); and an infinity or NaN in a
 // drafted V row is taken out of the product and added back only for the rows that attend to it.
 // ------------------------------------------------------------------------------------------
-
-// tanh on |x| <= kTanhNear as x p(x^2), p of degree 3 fitted for the least maximum relative error
-// (Lawson's reweighted least squares; 9.8e-08 in exact arithmetic). Scores of a capped head are mostly
-// this small, and five multiplications and additions on pairs of scores cost less than the general
-// form's two special-function calls each (three with the exponential, on a quarter-rate unit that
-// bounds wide drafts). The host folds the scales into the coefficients.
-constexpr float kTanhNear = 0.4f;
-constexpr double kTanh[4] = {0.999999901901, -0.333313624587, 0.132709767556, -0.0475536034831};
 
 template <int D, int TILES, bool CAP>
 __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2 : 1)
@@ -258,30 +407,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
 
     if (warp == 5 * TILES) {
         // ================================ producer warp ================================
-        auto state_of = [&](const TreeItem &it) {
-            ItemState s;
-            s.it = it;
-            const int32_t b = it.bh / a.Hkv;
-            s.tok0 = a.draft_off[b];
-            s.nb = a.draft_off[b + 1] - s.tok0;
-            s.len = a.kv_len[it.bh];
-            s.off = a.head_off[it.bh];
-            return s;
-        };
-        // the item after i of this worker: its own list, then tickets; -1 at the end
-        auto after = [&](int32_t i) {
-            if (i + 1 < i1) return i + 1;
-            if (n_static >= a.n_items) return -1;
-            int32_t k = 0;
-            if (lane == 0) k = static_cast<int32_t>(atomicAdd(a.ticket, 1u));
-            k = n_static + __shfl_sync(FULL, k, 0);
-            if (k >= a.n_items) return -1;
-            i1 = 0;  // from here on by ticket
-            return k;
-        };
-        int32_t cur = i0 < i1 ? i0 : after(i1 - 1);
-        ItemState nx{};
-        if (cur >= 0) nx = state_of(i0 < i1 ? first : a.items[cur]);
+        ItemWalk walk(a, i0, i1, n_static, first, lane);
         int32_t ent = 0, blk = 0, qn = 0, fills = 0;
         uint32_t eph = 1u;  // parity that says entry `ent` is free
         bool stop = *abort_flag != 0;
@@ -294,40 +420,17 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
             }
             return __shfl_sync(FULL, bad, 0) == 0;
         };
-        auto advance = [&]() {
-            cur = after(cur);
-            if (cur >= 0) nx = state_of(a.items[cur]);
-        };
-        while (cur >= 0 && !stop) {
-            const ItemState s = nx;
-            const int32_t b = s.it.bh / a.Hkv, h = s.it.bh - b * a.Hkv;
-            // a bad sequence or head is skipped whole: nothing of it is read
-            uint32_t err = 0;
-            if (s.nb < 0 || s.nb > a.max_draft || s.tok0 < 0 || static_cast<int64_t>(s.tok0) + s.nb > a.n_tokens) err |= kErrPlan;
-            if (s.len < 0 || s.len > s.it.cap) err |= kErrPlan;
-            const int32_t pages = (s.len + 15) / 16;
-            if (!err && pages > 0 && (s.off < a.row_lo[h] || s.off + pages > a.row_hi[h])) err |= kErrBadRow;
-            if (err) {
-                if (lane == 0) atomicOr(a.err, err);
-                advance();
+        while (walk.cur >= 0 && !stop) {
+            const ItemState s = walk.nx;
+            ItemShape sh;
+            if (!sh.of(a, s, kCutPages, lane)) {
+                walk.advance();
                 continue;
             }
-            const int32_t nrow = min(s.nb * a.G - s.it.row0, a.rows_item);
-            if (nrow <= 0) {
-                advance();
-                continue;
-            }
-            const int32_t np = max(0, min(s.it.page_end, pages) - s.it.page_begin);
-            const int32_t nc = (np + 3) / 4, nblk = nc + s.it.draft;
-            if (nblk == 0) {  // a part of a growing head that holds nothing yet
-                for (int32_t r = lane; r < nrow; r += 32)
-                    a.part_lse[static_cast<int64_t>(s.it.slot) * a.rows_item + r] = -INFINITY;
-                advance();
-                continue;
-            }
+            const int32_t h = sh.h, nrow = sh.nrow, np = sh.np, nc = sh.nc, nblk = nc + s.it.draft;
             // the next item is looked up while this one's blocks are in flight; a ticket is drawn late,
             // so that it is not held back from a CTA that is done earlier
-            const int32_t look = cur + 1 < i1 ? 0 : max(0, nblk - 2);
+            const int32_t look = walk.own_next() ? 0 : max(0, nblk - 2);
             const int32_t *row = a.table + s.off + s.it.page_begin;
             int32_t ids = lane < np ? __ldg(row + lane) : -1;
             int32_t ids_next = 32 + lane < np ? __ldg(row + 32 + lane) : -1;
@@ -419,7 +522,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
                     }
                     fill(true, p_draft, p_pid, p_boxes);
                 }
-                if (j == look) advance();
+                if (j == look) walk.advance();
             }
             if (!stop) {
                 if (wait_entry()) fill(true, is_draft, pid, boxes);
@@ -438,11 +541,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
                 mbar_wait(full + 8 * (f % NE), static_cast<uint32_t>(f / NE) & 1u, lim);
             for (int32_t k = max(0, qn - nq); k < qn; ++k)
                 mbar_wait(q_full + 8 * (k % nq), static_cast<uint32_t>(k / nq) & 1u, lim);
-            // the last CTA to come here readies the tickets for the next call
-            if (n_static < a.n_items && atomicAdd(a.ticket + 1, 1u) == gridDim.x - 1) {
-                a.ticket[0] = 0u;
-                a.ticket[1] = 0u;
-            }
+            walk.finish();
         }
         __syncwarp();
     } else if (warp >= 4 * TILES) {
@@ -582,73 +681,12 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
                 const int32_t v_fill = vh->v_fill, v_ent = v_fill >= NE ? v_fill - NE : v_fill;
                 ok = mbar_wait(full + 8 * v_ent, v_fill >= NE, a.wait_ns, abort_flag);
                 if (!__all_sync(FULL, ok)) { ok = false; break; }
-                const uint32_t v = ring + v_ent * TL::kEntry;
-                const int32_t end = (nv + 15) & ~15;
-                for (int32_t c = lane; c < (end - nv) * 8 * TL::kHalves; c += 32) {
-                    const int32_t r = nv + c / (8 * TL::kHalves), q = c % (8 * TL::kHalves);
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};"
-                                 ::"r"(v + (r >> 3) * TL::kGroup + (q >> 3) * 1024 + (r & 7) * 128 + (q & 7) * 16), "r"(0u) : "memory");
-                }
-                if (info & kDraft) {
-                    for (int32_t r = lane; r < nv; r += 32) {
-                        uint32_t seen = 0u;
-#pragma unroll
-                        for (int q = 0; q < 8 * TL::kHalves; ++q) {
-                            const uint32_t addr = v + (r >> 3) * TL::kGroup + (q >> 3) * 1024 + (r & 7) * 128 + (((q & 7) ^ (r & 7)) << 4);
-                            uint4 x;
-                            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(addr) : "memory");
-                            if (any_nonfinite(x.x) | any_nonfinite(x.y) | any_nonfinite(x.z) | any_nonfinite(x.w)) seen |= 1u << q;
-                        }
-                        if (seen) {
-                            atomicOr(&hd->bad, 1ull << r);
-                            __threadfence_block();
-                            for (int q = 0; q < 8 * TL::kHalves; ++q)
-                                if (seen >> q & 1u) {
-                                    const uint32_t addr = v + (r >> 3) * TL::kGroup + (q >> 3) * 1024 + (r & 7) * 128 + (((q & 7) ^ (r & 7)) << 4);
-                                    for (int w = 0; w < 8; ++w) {
-                                        uint16_t x;
-                                        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(addr + 2 * w) : "memory");
-                                        if ((x & 0x7F80u) == 0x7F80u)
-                                            asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr + 2 * w), "h"(static_cast<uint16_t>(0)) : "memory");
-                                    }
-                                }
-                        }
-                    }
-                }
-                fence_async_smem();
-                __syncwarp();
+                clean_v<TL::kHalves>(ring + v_ent * TL::kEntry, nv, info & kDraft, &hd->bad, lane);
             }
             tmem_wait_ld();
             float sl2 = CAP ? 1.f : a.scale_log2;
             if (CAP) {
-                // c tanh(x) in log2 units, x = s scale / c
-                float far = 0.f;
-#pragma unroll
-                for (int c = 0; c < 64; c += 2)
-                    far = max3(far, fabsf(__uint_as_float(sr[c])), fabsf(__uint_as_float(sr[c + 1])));
-                if (__all_sync(FULL, far * a.cap_x <= kTanhNear)) {
-                    const f2 c0 = pair(a.cap_p[0], a.cap_p[0]), c1 = pair(a.cap_p[1], a.cap_p[1]),
-                             c2 = pair(a.cap_p[2], a.cap_p[2]), c3 = pair(a.cap_p[3], a.cap_p[3]);
-#pragma unroll
-                    for (int c = 0; c < 64; c += 2) {
-                        const f2 x = pair(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
-                        const f2 y = mul2(x, x);
-                        const f2 p = mul2(x, fma2(fma2(fma2(c3, y, c2), y, c1), y, c0));
-                        float u, w;
-                        split(p, u, w);
-                        sr[c] = __float_as_uint(u);
-                        sr[c + 1] = __float_as_uint(w);
-                    }
-                } else {
-                    // tanh(x) = 1 - 2 / (1 + e^2x): absolute error of a few 2^-24 c, limits +-c
-                    const float k2 = 2.f * kLog2e * a.cap_x_signed;
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        const float e = ex2(__uint_as_float(sr[c]) * k2);
-                        sr[c] = __float_as_uint(a.cap2 * fmaf(-2.f, rcp(1.f + e), 1.f));
-                    }
-                }
+                cap_scores<64>(sr, a);
             } else if (sl2 < 0.f) {  // the maximum below is of the products: turn them under a negative scale
 #pragma unroll
                 for (int c = 0; c < 64; ++c) sr[c] ^= 0x80000000u;
@@ -796,6 +834,674 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
     fence_after();
     if (warp == 4 * TILES)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(TL::kCols) : "memory");
+}
+
+// ------------------------------------------------------------------------------------------
+// Narrow tree kernel (D = 128, up to 32 query rows: short drafts, and the single-token step), one
+// persistent CTA per SM. With few rows the wide kernel's 128-row products are mostly padding, which
+// costs power (its memory-bound steps ran at 1.5 GHz under the 1000 W cap), and one softmax thread
+// per row leaves most lanes idle. Here the products are turned over, so that tokens and head
+// dimensions fill the 128 lanes and the rows are the N side (NR = 16 or 32):
+//   S^T [128 tokens][NR] = K Q^T           (A = K, B = Q, both K-major in shared memory)
+//   O^T [128 dims][NR]  += V^T P^T         (A = V as stored, M-major; B = P^T, written to shared
+//                                           memory by the softmax threads, N-major)
+// A block is 128 tokens (8 pages). Blocks alternate between two streams with their own softmax
+// warpgroup, S and O in tensor memory, P buffer, and running maximum and sum, joined at the item's end.
+//   warps 0-3 / 4-7: softmax of the even / odd blocks; thread i owns token i of the block
+//   warp 8:          MMA issue (lane 0), tensor memory
+//   warp 9:          producer, as in the wide kernel; 32 KB ring entries
+// Softmax with a token per thread: the row's base m need not be its maximum, only near enough for
+// 2^(s - m) to stay in range, since floating point keeps the relative precision: m starts as the
+// score of the stream's first token and moves, with sums and O rescaled, only when a score exceeds
+// it by kNarrowSlack in log2 units (a score that stays below it is a true one, so the largest
+// probability is never under 1). Row sums stay in the threads, one per row, and are added across
+// threads once per item in a fixed order.
+// ------------------------------------------------------------------------------------------
+constexpr int kNBlock = 128;           // tokens of a block
+constexpr int kNPages = 8;
+constexpr float kNarrowSlack = 40.f;   // 2^40 times 2^30 tokens times |v| stays in fp32
+constexpr float kNoScore = -1e30f;     // base of a row that has seen no score
+
+template <int NR>
+struct NarrowLayout {
+    static constexpr int D = 128;
+    static constexpr int kEntry = kNBlock * D * 2;
+    static constexpr int kGroup = 2048;                   // 8 tokens: an atom per 64-column half
+    static constexpr int kQBox = NR * D * 2;
+    static constexpr int kQBoxes = 2;
+    static constexpr int kPitch = NR * 2;                 // bytes of a P row (a token)
+    static constexpr int kP = kNBlock * kPitch;
+    static constexpr int kMax = 6;                        // ring entries at most
+    // barriers: full[6], empty[6], q_full[2], q_empty[2], s_full[4], p_full[2], o_done[2], drain, join
+    static constexpr int kControl = kHdr * static_cast<int>(sizeof(BlockHdr)) + 2 * NR * 4 /* m */ + 2 * NR * 4 /* weights */ +
+                                    8 * (2 * kMax + 14) + 32;
+    static constexpr int kEntries = (227 * 1024 - kQBoxes * kQBox - 2 * kP - kControl) / kEntry;
+    static constexpr int kRing = kQBoxes * kQBox + 2 * kP;
+    static constexpr int kCtl = kRing + kEntries * kEntry;
+    static constexpr int kBytes = kCtl + kControl;
+    static constexpr int kThreads = 10 * 32;
+    static_assert(kEntries >= 4 && kEntries <= kMax, "ring entries");
+};
+
+// Order-preserving map of floats to unsigned integers (for integer maxima), and back.
+__device__ __forceinline__ uint32_t float_key(float x) {
+    const uint32_t u = __float_as_uint(x);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_float(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
+
+template <int NR, bool CAP>
+__global__ void __launch_bounds__(NarrowLayout<NR>::kThreads, 1)
+    tree_narrow_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap tm_q,
+                       const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CUtensorMap tm_kd, const __grid_constant__ CUtensorMap tm_vd) {
+    using NL = NarrowLayout<NR>;
+    using namespace ptx;
+    constexpr unsigned FULL = 0xffffffffu;
+    constexpr int D = 128, NE = NL::kEntries;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    const uint32_t sbase = smem_addr(smem);
+    const uint32_t ring = sbase + NL::kRing, pbuf = sbase + NL::kQBoxes * NL::kQBox;
+    BlockHdr *hdrs = reinterpret_cast<BlockHdr *>(smem + NL::kCtl);
+    float *base_m = reinterpret_cast<float *>(smem + NL::kCtl + kHdr * sizeof(BlockHdr));  // [2][NR]
+    float *weight = base_m + 2 * NR;                                                       // [2][NR]
+    const uint32_t full = smem_addr(weight + 2 * NR), empty = full + 8 * NL::kMax, q_full = empty + 8 * NL::kMax,
+                   q_empty = q_full + 16, s_full = q_empty + 16, p_full = s_full + 32, o_done = p_full + 16, drain = o_done + 16,
+                   join = drain + 8;
+    unsigned char *tail = smem + NL::kCtl + NL::kControl - 32;
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(tail);
+    volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tail + 4);
+    volatile int32_t *used = reinterpret_cast<volatile int32_t *>(tail + 8);                        // [2] stream has tokens
+    volatile unsigned long long *item_bad = reinterpret_cast<volatile unsigned long long *>(tail + 16);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int e = 0; e < NE; ++e) {
+            mbar_init(full + 8 * e, 1);
+            mbar_init(empty + 8 * e, 1);
+        }
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(q_full + 8 * k, 1);
+            mbar_init(q_empty + 8 * k, 1);
+            mbar_init(s_full + 8 * k, 1);
+            mbar_init(s_full + 16 + 8 * k, 1);
+            mbar_init(p_full + 8 * k, 4);
+            mbar_init(o_done + 8 * k, 1);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = (sbase & 1023u) ? 1 : 0;  // swizzled tiles need 1024-byte alignment
+        mbar_init(join, 8);
+        *item_bad = 0ull;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_addr(const_cast<uint32_t *>(tmem_slot))), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    // the plan's own lists do not change between calls: read before the preceding kernel is done
+    int32_t i0 = 0, i1 = 0, n_static = 0;
+    TreeItem first{};
+    if (warp == 9) {
+        i0 = a.worker_off[blockIdx.x];
+        i1 = a.worker_off[blockIdx.x + 1];
+        n_static = a.worker_off[gridDim.x];
+        if (i0 < i1) first = a.items[i0];
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_wait();
+    grid_launch();
+    auto timed_out = [&]() {
+        atomicOr(a.err, kErrTimeout);
+        *abort_flag = 1;
+    };
+
+    if (warp == 9) {
+        // ================================ producer warp ================================
+        ItemWalk walk(a, i0, i1, n_static, first, lane);
+        int32_t ent = 0, blk = 0, qn = 0, fills = 0;
+        uint32_t eph = 1u;
+        bool stop = *abort_flag != 0;
+        if (stop && lane == 0) atomicOr(a.err, kErrPlan);
+        auto wait_entry = [&]() {
+            int32_t bad = 0;
+            if (lane == 0 && !mbar_wait(empty + 8 * ent, eph, a.wait_ns, abort_flag)) {
+                timed_out();
+                bad = 1;
+            }
+            return __shfl_sync(FULL, bad, 0) == 0;
+        };
+        while (walk.cur >= 0 && !stop) {
+            const ItemState s = walk.nx;
+            ItemShape sh;
+            if (!sh.of(a, s, kNPages, lane)) {
+                walk.advance();
+                continue;
+            }
+            // every item has a block for each stream, if need be one without tokens
+            const int32_t nblk = max(2, sh.nc + s.it.draft);
+            const int32_t look = walk.own_next() ? 0 : max(0, nblk - 2);
+            const int32_t *row = a.table + s.off + s.it.page_begin;
+            int32_t ids = lane < sh.np ? __ldg(row + lane) : -1;
+            int32_t ids_next = 32 + lane < sh.np ? __ldg(row + 32 + lane) : -1;
+            const int qb = qn & 1;
+            // Fills go in the order of use: K(0), K(1), then K(j) and V(j - 2), then the last two V.
+            const int32_t fill0 = fills;
+            int32_t pid[3] = {0, 0, 0}, boxes[3] = {0, 0, 0};  // of blocks j, j - 1, j - 2
+            auto fill = [&](bool is_v, bool draft, int32_t page, int32_t n16) {
+                const uint32_t fb = full + 8 * ent;
+                if (lane == 0) {
+                    if (n16) mbar_expect_tx(fb, static_cast<uint32_t>(n16) * 16u * D * 2u);
+                    else mbar_arrive(fb);
+                }
+                __syncwarp();
+                if (lane < (draft ? 2 * n16 : n16)) {
+                    const uint32_t dst = ring + ent * NL::kEntry;
+                    if (draft) tma_4d(dst + lane * NL::kGroup, is_v ? &tm_vd : &tm_kd, 0, s.tok0 + 8 * lane, 0, sh.h, fb);
+                    else tma_4d(dst + lane * 2 * NL::kGroup, is_v ? &tm_v : &tm_k, 0, 0, 0, page * 2, fb);
+                }
+                ++fills;
+                if (++ent == NE) {
+                    ent = 0;
+                    eph ^= 1u;
+                }
+            };
+            for (int32_t j = 0; j < nblk && !stop; ++j, ++blk) {
+                pid[2] = pid[1];
+                pid[1] = pid[0];
+                boxes[2] = boxes[1];
+                boxes[1] = boxes[0];
+                const bool is_draft = s.it.draft && j == sh.nc;
+                int32_t nv = 0;
+                boxes[0] = 0;
+                if (is_draft) {
+                    nv = s.nb;
+                    boxes[0] = (nv + 15) / 16;
+                } else if (j < sh.nc) {
+                    boxes[0] = min(kNPages, sh.np - kNPages * j);
+                    nv = min(16 * boxes[0], s.len - 16 * (s.it.page_begin + kNPages * j));
+                    if (j > 0 && (j & 3) == 0) {
+                        ids = ids_next;
+                        ids_next = kNPages * j + 32 + lane < sh.np ? __ldg(row + kNPages * j + 32 + lane) : -1;
+                    }
+                }
+                pid[0] = __shfl_sync(FULL, ids, (kNPages * j + (lane & 7)) & 31);
+                if (!is_draft && lane < boxes[0] && (pid[0] < 0 || pid[0] >= a.num_pages)) {
+                    atomicOr(a.err, kErrBadPage);
+                    pid[0] = 0;  // a page of the pool; the row is flagged as unspecified
+                }
+                const bool last = j == nblk - 1;
+                if (!wait_entry()) {
+                    stop = true;
+                    break;
+                }
+                if (lane == 0) {
+                    BlockHdr *hd = hdrs + (blk % kHdr);
+                    // first and last block of each of the two streams
+                    hd->flags = (j < 2 ? kFirst : 0) | (j >= nblk - 2 ? kLast : 0) | (is_draft ? kDraft : 0) | (j == 0 ? kOpen : 0) |
+                                (last ? kClose : 0) | (s.it.draft ? kTakesDraft : 0) | (nv << 8) | (sh.nrow << 16);
+                    hd->tok0 = s.tok0;
+                    hd->h = sh.h;
+                    hd->slot = s.it.slot;
+                    hd->row0 = s.it.row0;
+                    hd->qb = static_cast<int16_t>(qb);
+                    hd->v_fill = static_cast<int16_t>((fill0 + (last ? 2 * nblk - 1 : j == nblk - 2 ? 2 * nblk - 2 : 2 * j + 3)) % (2 * NE));
+                    hd->bad = 0ull;
+                }
+                fill(false, is_draft, pid[0], boxes[0]);
+                if (j == 0) {
+                    // the item's query rows, into a box whose last scores are done
+                    int32_t bad = 0;
+                    if (lane == 0) {
+                        if (!mbar_wait(q_empty + 8 * qb, (static_cast<uint32_t>(qn >> 1) & 1u) ^ 1u, a.wait_ns, abort_flag)) {
+                            timed_out();
+                            bad = 1;
+                        } else {
+                            mbar_expect_tx(q_full + 8 * qb, NL::kQBox);
+#pragma unroll
+                            for (int qh = 0; qh < 2; ++qh)
+                                tma_3d(sbase + qb * NL::kQBox + qh * (NL::kQBox / 2), &tm_q, qh * 64, sh.h * a.G,
+                                       s.tok0 + (s.it.row0 >> a.g_shift), q_full + 8 * qb);
+                        }
+                    }
+                    if (__shfl_sync(FULL, bad, 0)) {
+                        stop = true;
+                        break;
+                    }
+                    ++qn;
+                } else if (j > 1) {
+                    if (!wait_entry()) {
+                        stop = true;
+                        break;
+                    }
+                    fill(true, false, pid[2], boxes[2]);
+                }
+                if (j == look) walk.advance();
+            }
+            // the drafted tokens, when the item takes them, are block nc (the last, or the last but one)
+            for (int32_t z = 1; z >= 0 && !stop; --z) {
+                if (wait_entry()) fill(true, s.it.draft && nblk - 1 - z == sh.nc, pid[z], boxes[z]);
+                else stop = true;
+            }
+        }
+        // an end marker for each stream; only the first takes a ring entry's turn
+        const bool ended = !stop && wait_entry();
+        if (ended && lane == 0) {
+            hdrs[blk % kHdr].flags = kStop;
+            hdrs[(blk + 1) % kHdr].flags = kStop;
+            mbar_arrive(full + 8 * ent);
+        }
+        if (lane == 0) {
+            // no copy may be in flight when the CTA exits
+            const uint64_t lim = a.wait_ns < kDrainNs ? a.wait_ns : kDrainNs;
+            for (int32_t f = max(0, fills - NE + (ended ? 1 : 0)); f < fills; ++f)
+                mbar_wait(full + 8 * (f % NE), static_cast<uint32_t>(f / NE) & 1u, lim);
+            for (int32_t k = max(0, qn - 2); k < qn; ++k)
+                mbar_wait(q_full + 8 * (k & 1), static_cast<uint32_t>(k >> 1) & 1u, lim);
+            walk.finish();
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // ================================ MMA warp ================================
+        // Order: S(blk), then the product of block blk - 2, so that a stream finds its next scores ready
+        // when it has finished a block. Each stream has two score buffers: S(blk) overwrites the scores
+        // of block blk - 4, which its softmax had read before that block's product was issued.
+        if (lane == 0) {
+            constexpr uint32_t hi_q = sdesc_hi(1024), hi_kv = sdesc_hi(NL::kGroup);
+            // P^T: 8 tokens of NR rows are an atom of 8 * kPitch bytes, swizzled by its row width
+            constexpr uint32_t hi_p = ((8 * NL::kPitch) >> 4) | (1u << 14) | ((NR == 32 ? 4u : 6u) << 29);
+            constexpr uint32_t id_s = idesc_bf16(NR, kRows, 0), id_o = idesc_bf16(NR, kRows, 1) | (1u << 15);
+            const uint32_t k_lo = sdesc_lo(ring, 16), v_lo = sdesc_lo(ring, 1024), q_lo = sdesc_lo(sbase, 16), p_lo = sdesc_lo(pbuf, 16);
+            bool ok = *abort_flag == 0;
+            int32_t qn = 0, ent = 0, p_info[2] = {0, 0};  // of blocks blk - 1, blk - 2
+            uint32_t eph = 0u;
+            auto next_entry = [&]() {
+                if (++ent == NE) {
+                    ent = 0;
+                    eph ^= 1u;
+                }
+            };
+            auto pv = [&](int32_t pb, int32_t info) {  // the product of block pb
+                const uint32_t st = pb & 1;
+                if (!mbar_wait(full + 8 * ent, eph, a.wait_ns, abort_flag) ||
+                    !mbar_wait(p_full + 8 * st, static_cast<uint32_t>(pb >> 1) & 1u, a.wait_ns, abort_flag))
+                    return false;
+                fence_after();
+                const int nk = (((info >> 8) & 0xFF) + 15) >> 4;
+                if (nk) {
+                    const uint32_t v = v_lo + ent * (NL::kEntry >> 4), p = p_lo + st * (NL::kP >> 4);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (k < nk)
+                            mma_ss(tmem + 256 + 64 * st, v + k * (2 * NL::kGroup >> 4), hi_kv, p + k * (16 * NL::kPitch >> 4), hi_p, id_o,
+                                   k > 0 || !(info & kFirst));
+                    mma_commit(o_done + 8 * st);
+                    mma_commit(empty + 8 * ent);
+                } else {
+                    mbar_arrive(o_done + 8 * st);
+                    mbar_arrive(empty + 8 * ent);
+                }
+                next_entry();
+                return true;
+            };
+            for (int32_t blk = 0; ok; ++blk) {
+                const uint32_t st = blk & 1;
+                // the ring brings an item's last two V before the next item's first K
+                if (p_info[0] & kClose) {
+                    if (!(ok = pv(blk - 2, p_info[1]) && pv(blk - 1, p_info[0]))) break;
+                }
+                ok = mbar_wait(full + 8 * ent, eph, a.wait_ns, abort_flag);
+                if (!ok) break;
+                const volatile BlockHdr *hd = hdrs + (blk % kHdr);
+                const int32_t info = hd->flags;
+                const uint32_t sb = 2 * st + ((blk >> 1) & 1);  // score buffer
+                if (info & kStop) {
+                    mbar_arrive(s_full + 8 * sb);
+                    mbar_arrive(s_full + 8 * (2 * (st ^ 1u) + (((blk + 1) >> 1) & 1)));
+                    break;
+                }
+                if (info & kOpen) {
+                    ok = mbar_wait(q_full + 8 * (qn & 1), static_cast<uint32_t>(qn >> 1) & 1u, a.wait_ns, abort_flag);
+                    if (!ok) break;
+                    ++qn;
+                }
+                fence_after();
+                if ((info >> 8) & 0xFF) {
+                    const uint32_t q = q_lo + ((qn - 1) & 1) * (NL::kQBox >> 4), k = k_lo + ent * (NL::kEntry >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_ss(tmem + 64 * sb, k + (ks / 4) * (1024 >> 4) + (ks % 4) * 2, hi_kv,
+                               q + (ks / 4) * (NL::kQBox / 2 >> 4) + (ks % 4) * 2, hi_q, id_s, ks > 0);
+                    mma_commit(s_full + 8 * sb);
+                    mma_commit(empty + 8 * ent);
+                } else {
+                    mbar_arrive(s_full + 8 * sb);
+                    mbar_arrive(empty + 8 * ent);
+                }
+                if (info & kClose) mma_commit(q_empty + 8 * ((qn - 1) & 1));
+                next_entry();
+                // an item's third block on: the one before the last
+                if (!(info & kOpen) && !(p_info[0] & kOpen) && !(ok = pv(blk - 2, p_info[1]))) break;
+                p_info[1] = p_info[0];
+                p_info[0] = info;
+            }
+            if (!ok) timed_out();
+            // every MMA of this thread has finished before tensor memory is released
+            mma_commit(drain);
+            mbar_wait(drain, 0, a.wait_ns < kDrainNs ? a.wait_ns : kDrainNs);
+        }
+        __syncwarp();
+    } else {
+        // ================================ softmax warpgroups ================================
+        const int st = warp >> 2, qd = warp & 3;
+        const int i = 32 * qd + lane;  // token of the block; lane of tensor memory
+        const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
+        const uint32_t t_o = tmem + lanes + 256;
+        const uint32_t p_row = pbuf + st * NL::kP + i * NL::kPitch;
+        // 16-byte chunk of a P row under the row width's swizzle
+        const uint32_t p_xor = NR == 32 ? ((i >> 1) & 3) : ((i >> 2) & 1);
+        float *m_row = base_m + st * NR;
+        f2 le[NR / 2];
+        bool ok = *abort_flag == 0;
+        auto wg_sync = [&]() { asm volatile("bar.sync %0, 128;" ::"r"(1 + st) : "memory"); };
+        // both warpgroups meet; bounded, since one of them may have given up
+        uint32_t jph = 0u;
+        auto both_sync = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(join);
+            if (!mbar_wait(join, jph, a.wait_ns, abort_flag)) ok = false;
+            jph ^= 1u;
+            __syncwarp();
+        };
+        auto wg_any = [&](bool v) {
+            uint32_t r;
+            asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbar.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                         : "=r"(r) : "r"(1 + st), "r"(static_cast<uint32_t>(v)) : "memory");
+            return r != 0;
+        };
+        for (int32_t blk = st;; blk += 2) {
+            const uint32_t ph = static_cast<uint32_t>(blk >> 1) & 1u;
+            // the warpgroup's barriers count all its threads, so they take every branch around them
+            // together, and after a failure leave together here
+            const uint32_t sb = 2 * st + ((blk >> 1) & 1);
+            const uint32_t t_s = tmem + lanes + 64 * sb;
+            ok = !wg_any(!ok || !mbar_wait(s_full + 8 * sb, static_cast<uint32_t>(blk >> 2) & 1u, a.wait_ns, abort_flag));
+            if (!ok) break;
+            fence_after();
+            BlockHdr *hd = hdrs + (blk % kHdr);
+            const volatile BlockHdr *vh = hd;
+            const int32_t info = vh->flags;
+            if (info & kStop) break;
+            const int32_t nv = (info >> 8) & 0xFF, nrow = info >> 16;
+            if (info & kFirst) {
+#pragma unroll
+                for (int r = 0; r < NR / 2; ++r) le[r] = pair(0.f, 0.f);
+                if (i == 0) used[st] = nv > 0;
+                if (nv == 0 && i < NR) m_row[i] = kNoScore;
+            }
+            if (nv > 0) {
+                uint32_t sr[NR];
+                tmem_ld<NR>(t_s, sr);
+                // V rows between the valid tokens and the end of their 16-row box, and infinities and NaN
+                // of drafted V rows, leave the product (see the wide kernel)
+                if (qd == 0 && ((nv & 15) || (info & kDraft))) {
+                    const int32_t v_fill = vh->v_fill, v_ent = v_fill >= NE ? v_fill - NE : v_fill;
+                    ok = mbar_wait(full + 8 * v_ent, v_fill >= NE, a.wait_ns, abort_flag);
+                    ok = __all_sync(FULL, ok);
+                    if (ok) clean_v<2>(ring + v_ent * NL::kEntry, nv, info & kDraft, &hd->bad, lane);
+                }
+                // rows that this thread's token counts for
+                uint32_t sees = i < nv ? ~0u : 0u;
+                if (info & kDraft) {
+                    sees = 0u;
+                    if (i < nv) {
+                        const unsigned long long *mk = a.mask + vh->tok0 + (vh->row0 >> a.g_shift);
+                        const uint32_t group = (1u << a.G) - 1u;
+#pragma unroll 4
+                        for (int32_t r = 0; r < nrow; r += a.G)
+                            if (__ldg(mk + (r >> a.g_shift)) >> i & 1ull) sees |= group << r;
+                    }
+                }
+                const bool masked = __any_sync(FULL, (info & kDraft) || i >= nv);
+                const bool in_box = i < ((nv + 15) & ~15);
+                tmem_wait_ld();
+                float *m = m_row;
+                float sl2 = a.scale_log2;
+                if (CAP) {
+                    cap_scores<NR>(sr, a);
+                    sl2 = 1.f;
+                }
+                if (masked) {  // scores times scale, -inf where they do not count
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) sr[r] = __float_as_uint((sees >> r & 1u) ? __uint_as_float(sr[r]) * sl2 : -INFINITY);
+                    sl2 = 1.f;
+                }
+                if (info & kFirst) {
+                    // a base to start with: the first token's score, which counts for every row; drafted
+                    // tokens do not, so there the base is found below
+                    if (info & kDraft) {
+                        if (i < NR) m[i] = kNoScore;
+                    } else if (i == 0) {
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) {
+                            const float x = __uint_as_float(sr[r]) * sl2;
+                            m[r] = x == -INFINITY ? kNoScore : x;
+                        }
+                    }
+                    wg_sync();
+                }
+                const f2 k = pair(sl2, sl2);
+                float top = -INFINITY;
+#pragma unroll
+                for (int r = 0; r < NR; r += 4) {
+                    const float4 mm = *reinterpret_cast<const float4 *>(m + r);
+                    float t0, t1, t2, t3;
+                    split(fma2(pair(__uint_as_float(sr[r]), __uint_as_float(sr[r + 1])), k, pair(-mm.x, -mm.y)), t0, t1);
+                    split(fma2(pair(__uint_as_float(sr[r + 2]), __uint_as_float(sr[r + 3])), k, pair(-mm.z, -mm.w)), t2, t3);
+                    top = max3(max3(top, t0, t1), t2, t3);
+                }
+                if (wg_any(top > kNarrowSlack)) {
+                    // Far above the base: the base moves to the exact maximum, sums and O with it. Rare, so
+                    // small code: the scores are read again, 8 rows at a time.
+                    uint32_t *key = reinterpret_cast<uint32_t *>(weight + st * NR);
+                    if (i < NR) key[i] = float_key(m[i] == m[i] ? m[i] : kNoScore);
+                    wg_sync();
+#pragma unroll 1
+                    for (int r8 = 0; r8 < NR; r8 += 8) {
+                        uint32_t x[8];
+                        tmem_ld<8>(t_s + r8, x);
+                        tmem_wait_ld();
+                        if (CAP) cap_scores<8>(x, a);
+                        const uint32_t on = sees >> r8;
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const float y = __uint_as_float(x[r]) * (CAP ? 1.f : a.scale_log2);
+                            const uint32_t u = __reduce_max_sync(FULL, float_key((on >> r & 1u) && y > kNoScore ? y : kNoScore));
+                            if (lane == 0) atomicMax(key + r8 + r, u);
+                        }
+                    }
+                    wg_sync();
+                    float factor = 0.f, moved = 0.f;
+                    if (i < NR) {
+                        moved = m[i] == m[i] ? key_float(key[i]) : m[i];
+                        factor = ex2(m[i] - moved);
+                    }
+                    wg_sync();
+                    if (i < NR) {
+                        m[i] = moved;
+                        weight[st * NR + i] = factor;
+                    }
+                    wg_sync();
+                    const float *f = weight + st * NR;
+                    if (!(info & kFirst)) {
+                        // the stream's last product is done before O is scaled
+                        if (!mbar_wait(o_done + 8 * st, ph ^ 1u, a.wait_ns, abort_flag)) ok = false;
+                        fence_after();
+#pragma unroll 1
+                        for (int r8 = 0; r8 < NR; r8 += 8) {
+                            uint32_t o[8];
+                            tmem_ld<8>(t_o + 64 * st + r8, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int r = 0; r < 8; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f[r8 + r]);
+                            tmem_st8(t_o + 64 * st + r8, o);
+                        }
+                        tmem_wait_st();
+                    }
+#pragma unroll
+                    for (int r = 0; r < NR / 2; ++r)
+                        le[r] = mul2(le[r], pair(f[2 * r], f[2 * r + 1]));
+                    wg_sync();
+                }
+                // the P buffer's last reader is done
+                if (!(info & kFirst) && !mbar_wait(o_done + 8 * st, ph ^ 1u, a.wait_ns, abort_flag)) ok = false;
+#pragma unroll
+                for (int r = 0; r < NR; r += 8) {
+                    uint32_t pw[4];
+#pragma unroll
+                    for (int c = 0; c < 8; c += 4) {
+                        const float4 mm = *reinterpret_cast<const float4 *>(m + r + c);
+                        float p0, p1, p2, p3;
+                        split(fma2(pair(__uint_as_float(sr[r + c]), __uint_as_float(sr[r + c + 1])), k, pair(-mm.x, -mm.y)), p0, p1);
+                        split(fma2(pair(__uint_as_float(sr[r + c + 2]), __uint_as_float(sr[r + c + 3])), k, pair(-mm.z, -mm.w)), p2, p3);
+                        p0 = ex2(p0);
+                        p1 = ex2(p1);
+                        p2 = ex2(p2);
+                        p3 = ex2(p3);
+                        const int at = (r + c) / 2;
+                        le[at] = add2(le[at], pair(p0, p1));
+                        le[at + 1] = add2(le[at + 1], pair(p2, p3));
+                        pw[c / 2] = pack_bf16(p0, p1);
+                        pw[c / 2 + 1] = pack_bf16(p2, p3);
+                    }
+                    if (in_box)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                                     ::"r"(p_row + (((r / 8) ^ p_xor) << 4)), "r"(pw[0]), "r"(pw[1]), "r"(pw[2]), "r"(pw[3]) : "memory");
+                }
+                fence_async_smem();
+            }
+            fence_before();
+            __syncwarp();
+            if (info & kDraft) {  // for the rows' corrections below
+                wg_sync();
+                if (i == 0) *item_bad = *const_cast<volatile unsigned long long *>(&hd->bad);
+            }
+            if (!__all_sync(FULL, ok)) ok = false;
+            if (lane == 0 && ok) mbar_arrive(p_full + 8 * st);
+            if (!(info & kLast)) continue;
+
+            // ---- the item's rows ----
+            const int32_t tok0 = vh->tok0, h = vh->h, slot = vh->slot, row0 = vh->row0;
+            if (wg_any(!ok || !mbar_wait(o_done + 8 * st, ph, a.wait_ns, abort_flag))) ok = false;
+            fence_after();
+            // row sums over the warp's tokens: halves of the rows change sides with the lanes, so that
+            // NR values need about NR shuffles, not 5 NR; lane l ends with rows of index bits from l
+            float v[NR];
+#pragma unroll
+            for (int r = 0; r < NR / 2; ++r) split(le[r], v[2 * r], v[2 * r + 1]);
+            constexpr int STEPS = NR >= 32 ? 5 : 4;
+#pragma unroll
+            for (int z = 0; z < STEPS; ++z) {
+                const int half = NR >> (z + 1);
+                const bool up = lane >> z & 1;
+#pragma unroll
+                for (int r = 0; r < half; ++r) {
+                    const float mine = up ? v[r + half] : v[r], other = up ? v[r] : v[r + half];
+                    v[r] = mine + __shfl_xor_sync(FULL, other, 1 << z);
+                }
+            }
+            if (NR == 16) v[0] += __shfl_xor_sync(FULL, v[0], 16);
+            // lane l holds row sum_z bit_z(l) NR / 2^(z + 1)
+            int32_t r_at = 0;
+#pragma unroll
+            for (int z = 0; z < STEPS; ++z) r_at += (lane >> z & 1) * (NR >> (z + 1));
+            // the stream's P buffer is free: the warps' sums, joined in warp order
+            float *sums = reinterpret_cast<float *>(smem + NL::kQBoxes * NL::kQBox + st * NL::kP);  // [4][NR]
+            if (lane < NR) sums[qd * NR + r_at] = v[0];
+            both_sync();
+            // this warpgroup's half of the rows: weights of the two streams, lse
+            constexpr int HR = NR / 2;
+            const int32_t r_lo = st * HR;
+            if (i < HR) {
+                const int32_t r = r_lo + i;
+                const float *s0 = reinterpret_cast<const float *>(smem + NL::kQBoxes * NL::kQBox), *s1 = s0 + NL::kP / 4;
+                const float l0 = (s0[r] + s0[NR + r]) + (s0[2 * NR + r] + s0[3 * NR + r]);
+                const float l1 = (s1[r] + s1[NR + r]) + (s1[2 * NR + r] + s1[3 * NR + r]);
+                const float m0 = base_m[r], m1 = base_m[NR + r];
+                const float M = m0 != m0 || m1 != m1 ? NAN : fmaxf(m0, m1);
+                const float e0 = ex2(m0 - M), e1 = ex2(m1 - M);
+                const float L = l0 * e0 + l1 * e1;
+                const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
+                weight[r] = used[0] ? e0 * inv : 0.f;
+                weight[NR + r] = used[1] ? e1 * inv : 0.f;
+                if (r < nrow) {
+                    const float l = L == 0.f ? -INFINITY : (M + lg2(L)) * kLn2;
+                    const int32_t q = row0 + r;
+                    if (slot < 0) a.lse[static_cast<int64_t>(tok0 + (q >> a.g_shift)) * a.Hq + h * a.G + (q & (a.G - 1))] = l;
+                    else a.part_lse[static_cast<int64_t>(slot) * a.rows_item + r] = l;
+                }
+            }
+            wg_sync();
+            const unsigned long long bad = (info & kTakesDraft) ? *item_bad : 0ull;
+            const bool u0 = used[0], u1 = used[1];
+            // out^T = w0 O0^T + w1 O1^T; thread i holds dimension i, so a warp writes 32 consecutive elements
+            // of a row at a time
+            constexpr int C = HR < 16 ? HR : 16;
+#pragma unroll 1
+            for (int r8 = 0; r8 < HR && r_lo + r8 < nrow; r8 += C) {
+                uint32_t oa[C], ob[C];
+                tmem_ld<C>(t_o + r_lo + r8, oa);
+                tmem_ld<C>(t_o + 64 + r_lo + r8, ob);
+                tmem_wait_ld();
+                float x[C];
+#pragma unroll
+                for (int r = 0; r < C; ++r) {
+                    const int32_t rr = r_lo + r8 + r;
+                    x[r] = (u0 ? __uint_as_float(oa[r]) * weight[rr] : 0.f) + (u1 ? __uint_as_float(ob[r]) * weight[NR + rr] : 0.f);
+                }
+                if (bad) {
+#pragma unroll 1
+                    for (int r = 0; r < C && r_lo + r8 + r < nrow; ++r) {
+                        unsigned long long rest = bad & __ldg(a.mask + tok0 + ((row0 + r_lo + r8 + r) >> a.g_shift));
+                        float add = 0.f;
+                        for (; rest; rest &= rest - 1) {
+                            const int j = __ffsll(static_cast<long long>(rest)) - 1;
+                            const float y = __bfloat162float(a.v_draft[(static_cast<int64_t>(tok0) + j) * a.v_stride + h * D + i]);
+                            if (!isfinite(y)) add += y;
+                        }
+#pragma unroll
+                        for (int q = 0; q < C; ++q) x[q] = q == r ? x[q] + add : x[q];
+                    }
+                }
+                if (slot < 0) {
+#pragma unroll
+                    for (int r = 0; r < C; ++r) {
+                        const int32_t q = row0 + r_lo + r8 + r;
+                        if (r_lo + r8 + r < nrow)
+                            a.out[(static_cast<int64_t>(tok0 + (q >> a.g_shift)) * a.Hq + h * a.G + (q & (a.G - 1))) * D + i] = __float2bfloat16_rn(x[r]);
+                    }
+                } else {
+                    float *po = a.part_o + (static_cast<int64_t>(slot) * a.rows_item + r_lo + r8) * D + i;
+#pragma unroll
+                    for (int r = 0; r < C; ++r)
+                        if (r_lo + r8 + r < nrow) po[r * D] = x[r];
+                }
+            }
+            fence_before();
+            both_sync();  // O, the sums and the item's mask are free for the next item
+            fence_after();
+        }
+        if (!ok && lane == 0) timed_out();
+    }
+    // all warps meet before tensor memory is released
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == 8)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
 // ------------------------------------------------------------------------------------------
@@ -959,9 +1665,12 @@ int token_map(CUtensorMap *tm, const void *base, int32_t D, int32_t heads, int64
 
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-constexpr int kItemCost = 12;  // pages' worth of an item's fixed work (draft block, Q, output)
+// Pages' worth of an item's fixed work (draft block, Q, joining, output): the wide kernel's and the
+// narrow one's, and the shares of the cost laid out ahead of time. Measured per item on the serving
+// layer: 3 us and 4.5 us, against 0.4 us and 0.18 us a page.
+constexpr int kItemCost = 12, kItemCostNarrow = 24;
 constexpr int kMinShare = 16;  // no worker's share below this many pages' worth
-constexpr int kStaticPermille = 950;
+constexpr int kStaticPermille = 950, kStaticPermilleNarrow = 900;
 
 // Work list. A unit is a (head, row block): a run of pages plus a fixed cost. Units are taken longest
 // first; the first kStaticPermille of the cost is laid end to end and cut into equal shares, one per
@@ -977,11 +1686,15 @@ void build_items(tg_tree_plan *p, const int32_t *cap, int32_t num_workers) {
     for (int64_t i = 0; i < BH; ++i) order[static_cast<size_t>(i)] = static_cast<int32_t>(i);
     std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return cap[x] > cap[y]; });
     int64_t total = 0;
-    for (int64_t i = 0; i < BH; ++i) total += (cap[i] + 15) / 16 + kItemCost;
+    const int32_t item_cost = p->narrow ? kItemCostNarrow : kItemCost;
+    for (int64_t i = 0; i < BH; ++i) total += (cap[i] + 15) / 16 + item_cost;
     total *= rblocks;
     const int64_t nw = std::max<int64_t>(1, std::min<int64_t>(num_workers, total / kMinShare));
-    const int64_t fixed = nw == num_workers && nw > 1 && p->tiles == 1 ? total * kStaticPermille / 1000 : total;
-    const int64_t min_dyn = std::max<int64_t>(16, p->rows_item / 4 / kCutPages * kCutPages);
+    const int64_t fixed = nw == num_workers && nw > 1 && p->tiles == 1
+                              ? total * (p->narrow ? kStaticPermilleNarrow : kStaticPermille) / 1000
+                              : total;
+    const int32_t cut = p->narrow ? kNPages : kCutPages;  // heads are cut at whole blocks
+    const int64_t min_dyn = p->narrow ? 32 : std::max<int64_t>(16, p->rows_item / 4 / cut * cut);
     p->worker_off.assign(1, 0);
     int64_t done = 0;  // cost laid out so far
     int64_t w = 1;     // the current worker's share ends at fixed * w / nw
@@ -994,20 +1707,20 @@ void build_items(tg_tree_plan *p, const int32_t *cap, int32_t num_workers) {
             for (;;) {
                 int64_t room;  // pages this item may take
                 // the share is full when what is left of it would hold less than a block
-                while (w <= nw && done + (at == 0 ? kItemCost : 0) + kCutPages > fixed * w / nw) {
+                while (w <= nw && done + (at == 0 ? item_cost : 0) + cut > fixed * w / nw) {
                     if (w == nw && fixed == total) break;  // all static: the last worker takes the rest
                     p->worker_off.push_back(static_cast<int32_t>(p->items.size()));
                     ++w;
                 }
                 if (w <= nw) {
-                    room = w == nw && fixed == total ? INT_MAX : fixed * w / nw - done - (at == 0 ? kItemCost : 0);
+                    room = w == nw && fixed == total ? INT_MAX : fixed * w / nw - done - (at == 0 ? item_cost : 0);
                 } else {
                     room = std::max<int64_t>(min_dyn, (total - done) / (2 * nw));
                     if (pages - at <= room + room / 2) room = pages - at;
                 }
-                room = std::max<int64_t>(kCutPages, room / kCutPages * kCutPages);
+                room = std::max<int64_t>(cut, room / cut * cut);
                 int32_t end = static_cast<int32_t>(std::min<int64_t>(pages, at + room));
-                if (pages - end < 2 * kCutPages) end = pages;  // no sliver of a head for the next worker
+                if (pages - end < 2 * cut) end = pages;  // no sliver of a head for the next worker
                 TreeItem it{};
                 it.bh = i;
                 it.page_begin = at;
@@ -1017,7 +1730,7 @@ void build_items(tg_tree_plan *p, const int32_t *cap, int32_t num_workers) {
                 it.cap = cap[i];
                 it.slot = -1;
                 p->items.push_back(it);
-                done += (end - at) + (at == 0 ? kItemCost : 0);
+                done += (end - at) + (at == 0 ? item_cost : 0);
                 at = end;
                 if (at == pages) break;
             }
@@ -1049,6 +1762,14 @@ int set_smem_both() {
     return rc != TG_OK ? rc : set_smem<D, TILES, true>();
 }
 
+template <int NR>
+int set_smem_narrow_t() {
+    TG_TRY(cudaFuncSetAttribute(tree_narrow_kernel<NR, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, NarrowLayout<NR>::kBytes));
+    TG_TRY(cudaFuncSetAttribute(tree_narrow_kernel<NR, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, NarrowLayout<NR>::kBytes));
+    return TG_OK;
+}
+int set_smem_narrow(int32_t nr) { return nr == 16 ? set_smem_narrow_t<16>() : set_smem_narrow_t<32>(); }
+
 // Selects the plan's device for a scope and puts the caller's back.
 struct DeviceScope {
     int before = -1, now = -1;
@@ -1066,7 +1787,8 @@ struct DeviceScope {
 int tree_device_init(tg_tree_plan *p) {
     DeviceScope scope;
     TG_TRY(scope.enter(p->device));
-    const int rc = p->shape.D == 128 ? (p->tiles == 1 ? set_smem_both<128, 1>() : set_smem_both<128, 2>())
+    const int rc = p->narrow         ? set_smem_narrow(p->narrow)
+                   : p->shape.D == 128 ? (p->tiles == 1 ? set_smem_both<128, 1>() : set_smem_both<128, 2>())
                                      : (p->tiles == 1 ? set_smem_both<64, 1>() : set_smem_both<64, 2>());
     if (rc != TG_OK) return rc;
     int64_t at = 0;
@@ -1167,7 +1889,19 @@ int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft
     p->q_rows = p->tiles == 2 ? kRows : (max_draft * G + 7) / 8 * 8;
     // a second Q box lets the next item's queries load beside the current one's, where it costs at
     // most one ring entry
-    if (s->D == 128)
+    // The narrow kernel, whose items cost more and whose tokens cost less, from the mean pages of a head
+    // on at which it measured faster (256 or 128 sequences of 32/8 heads, us narrow : wide, by mean pages).
+    // 4 to 16 rows:  8: 104 : 87   23: 124 : 131   45: 175 : 184   90: 144 : 146   180: 259 : 314
+    // 32 rows:       8: 125 : 97   23: 168 : 151   45: 232 : 208   90: 174 : 170   180: 286 : 308
+    // (64 rows of a variant with NR = 64: 180: 199 : 134, its softmax no longer hidden by the loads.)
+    int64_t pages = 0;
+    for (int64_t i = 0; i < BH; ++i) pages += (kv_cap[i] + 15) / 16;
+    const int32_t rows = max_draft * G;
+    if (s->D == 128 && rows <= 32 && pages >= BH * (rows <= 16 ? 16 : 112)) {
+        p->narrow = rows <= 16 ? 16 : 32;
+        p->q_rows = p->narrow;
+        p->smem_bytes = p->narrow == 16 ? NarrowLayout<16>::kBytes : NarrowLayout<32>::kBytes;
+    } else if (s->D == 128)
         p->tiles == 1 ? set_geometry<128, 1>(p.get()) : set_geometry<128, 2>(p.get());
     else
         p->tiles == 1 ? set_geometry<64, 1>(p.get()) : set_geometry<64, 2>(p.get());
@@ -1184,8 +1918,8 @@ int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft
         const int rc = device_num_sms(p->device, &sms);
         if (rc != TG_OK) return rc;
     }
-    // one resident wave: two CTAs per SM with one tile, one CTA with two
-    const int32_t resident = sms * (p->tiles == 1 ? 2 : 1);
+    // one resident wave: two CTAs per SM of the wide kernel with one tile, else one
+    const int32_t resident = sms * (p->tiles == 1 && !p->narrow ? 2 : 1);
     build_items(p.get(), kv_cap, num_workers > 0 ? num_workers : resident);
     if (!p->host_only) {
         const int rc = tree_device_init(p.get());
@@ -1195,12 +1929,12 @@ int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft
     return TG_OK;
 }
 
-template <int D, int TILES, bool CAP>
-int launch_tree(const tg_tree_plan *p, const TreeArgs &a, const CUtensorMap *tm, cudaStream_t stream) {
-    using TL = TreeLayout<D, TILES>;
+typedef void (*TreeFn)(TreeArgs, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap);
+
+int launch_tree(const tg_tree_plan *p, TreeFn fn, int threads, const TreeArgs &a, const CUtensorMap *tm, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p->n_workers));
-    cfg.blockDim = dim3(TL::kThreads);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = static_cast<size_t>(p->smem_bytes);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -1208,14 +1942,27 @@ int launch_tree(const tg_tree_plan *p, const TreeArgs &a, const CUtensorMap *tm,
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    TG_TRY(cudaLaunchKernelEx(&cfg, tree_kernel<D, TILES, CAP>, a, tm[0], tm[1], tm[2], tm[3], tm[4]));
+    TG_TRY(cudaLaunchKernelEx(&cfg, fn, a, tm[0], tm[1], tm[2], tm[3], tm[4]));
     return TG_OK;
 }
 
-template <int D>
-int launch_tree_d(const tg_tree_plan *p, const TreeArgs &a, const CUtensorMap *tm, bool cap, cudaStream_t stream) {
-    if (p->tiles == 1) return cap ? launch_tree<D, 1, true>(p, a, tm, stream) : launch_tree<D, 1, false>(p, a, tm, stream);
-    return cap ? launch_tree<D, 2, true>(p, a, tm, stream) : launch_tree<D, 2, false>(p, a, tm, stream);
+template <int NR>
+TreeFn narrow_fn(bool cap) {
+    return cap ? tree_narrow_kernel<NR, true> : tree_narrow_kernel<NR, false>;
+}
+
+int launch_tree_kernel(const tg_tree_plan *p, const TreeArgs &a, const CUtensorMap *tm, bool cap, cudaStream_t stream) {
+    if (p->narrow)
+        return launch_tree(p, p->narrow == 16 ? narrow_fn<16>(cap) : narrow_fn<32>(cap),
+                           NarrowLayout<32>::kThreads, a, tm, stream);
+    if (p->shape.D == 128) {
+        if (p->tiles == 1)
+            return launch_tree(p, cap ? tree_kernel<128, 1, true> : tree_kernel<128, 1, false>, TreeLayout<128, 1>::kThreads, a, tm, stream);
+        return launch_tree(p, cap ? tree_kernel<128, 2, true> : tree_kernel<128, 2, false>, TreeLayout<128, 2>::kThreads, a, tm, stream);
+    }
+    if (p->tiles == 1)
+        return launch_tree(p, cap ? tree_kernel<64, 1, true> : tree_kernel<64, 1, false>, TreeLayout<64, 1>::kThreads, a, tm, stream);
+    return launch_tree(p, cap ? tree_kernel<64, 2, true> : tree_kernel<64, 2, false>, TreeLayout<64, 2>::kThreads, a, tm, stream);
 }
 
 template <int D>
@@ -1253,8 +2000,9 @@ extern "C" void tg_tree_plan_destroy(tg_tree_plan *p) {
 }
 
 extern "C" int tg_tree_plan_items(const tg_tree_plan *p, int32_t *n_items, int32_t *n_workers, int32_t *n_merge,
-                                  int64_t *device_bytes, int32_t *items, int32_t *worker_off) {
+                                  int32_t *rows, int64_t *device_bytes, int32_t *items, int32_t *worker_off) {
     if (!p) return TG_EINVAL;
+    if (rows) *rows = p->narrow ? p->narrow : kRows * p->tiles;
     if (n_items) *n_items = static_cast<int32_t>(p->items.size());
     if (n_workers) *n_workers = p->n_workers;
     if (n_merge) *n_merge = static_cast<int32_t>(p->merge.size());
@@ -1346,7 +2094,7 @@ extern "C" int tg_tree_decode(tg_tree_plan *p, int64_t n_tokens, const int32_t *
     a.part_lse = p->d_part_lse;
     a.err = p->d_err;
     a.wait_ns = p->wait_ns;
-    rc = s.D == 128 ? launch_tree_d<128>(p, a, tm, softcap > 0.f, st) : launch_tree_d<64>(p, a, tm, softcap > 0.f, st);
+    rc = launch_tree_kernel(p, a, tm, softcap > 0.f, st);
     if (rc != TG_OK || p->merge.empty()) return rc;
     TreeMergeArgs g{};
     g.merge = p->d_merge;

@@ -18,8 +18,15 @@ class Batch:
     """A random ragged batch on the GPU with its plan."""
 
     def __init__(self, seed, G, D, Hkv, lens, nd, max_draft=None, cap_extra=0, workers=0, q_scale=1.5, stale=0.0,
-                 extra_rows=0, masks=None, fused=True):
+                 extra_rows=0, masks=None, fused=True, few=False):
         rng = np.random.default_rng(seed)
+        if few:  # one more sequence, long enough for the kernel that few rows and long heads take
+            units = np.size(lens) // Hkv + 1
+            lens = np.concatenate([np.ravel(lens), np.full(Hkv, 120 * 16 * units - 7)])
+            nd = np.concatenate([nd, [1]])
+            max_draft = max_draft or int(np.max(nd))
+            if masks is not None:
+                masks = list(masks) + [1]
         self.G, self.D, self.Hkv, self.Hq = G, D, Hkv, G * Hkv
         self.lens = np.asarray(lens, np.int64).reshape(-1)
         self.B = self.lens.size // Hkv
@@ -48,6 +55,8 @@ class Batch:
         self.plan = tg.tg_tree_plan_create(self.shape, cap, max_draft or max(1, int(self.nd.max(initial=1))),
                                            np.zeros(Hkv, np.int32), [0, max(1, self.ids.size)], num_workers=workers,
                                            wait_limit_us=1000000)
+        self.rows = tg.tg_tree_plan_items(self.plan)["rows"]
+        assert not few or self.rows == (16 if G * max_draft <= 16 else 32)
         self.scale = 1 / math.sqrt(D)
         self.dev = dict(kp=self.k_pages.cuda(), vp=self.v_pages.cuda(),
                         table=torch.from_numpy(self.ids if self.ids.size else np.zeros(1, np.int32)).cuda(),
@@ -102,11 +111,23 @@ def test_shapes(D, G, T):
     bt.check()
 
 
+@pytest.mark.parametrize("G,T", [(1, 1), (1, 16), (1, 29), (2, 8), (4, 1), (4, 4), (4, 5), (4, 8), (8, 2), (8, 4)])
+def test_shapes_of_few_rows(G, T):
+    """The same for the kernel of few rows and long heads: lengths of none to several blocks beside a
+    long one, ragged drafts."""
+    rng = np.random.default_rng(10 * G + T)
+    bt = Batch(G + T, G, 128, 2, rng.choice(LENGTHS, size=8), [T, 0, max(1, T // 2), int(rng.integers(0, T + 1))], max_draft=T,
+               few=True)
+    bt.run()
+    bt.check()
+
+
 @pytest.mark.parametrize("workers", [1, 3, 0])
-def test_lengths_and_splits(workers):
+@pytest.mark.parametrize("few", [False, True])
+def test_lengths_and_splits(workers, few):
     """Lengths around page and block ends, whole and split heads (merged in order)."""
     lens = LENGTHS + [700, 1023]
-    bt = Batch(5, 4, 128, 2, lens, [3, 0, 7, 1, 2, 16, 4], workers=workers)
+    bt = Batch(5, 4, 128, 2, lens, [3, 0, 7, 1, 2, 8 if few else 16, 4], workers=workers, few=few)
     bt.run()
     bt.check()
 
@@ -118,6 +139,28 @@ def test_split_heads_of_long_rows():
     bt.check()
 
 
+@pytest.mark.parametrize("G,T", [(4, 4), (4, 8), (4, 16), (4, 40), (1, 3)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rising", [True, False])
+@pytest.mark.parametrize("few", [False, True])
+def test_scores_far_from_the_first(G, T, D, rising, few):
+    """Scores that climb by hundreds over a head's tokens (every block moves the running base), or that
+    fall from a first token far above the rest; drafted keys above all of them."""
+    if few and (D == 64 or G * T > 32):
+        pytest.skip("not a shape of the kernel of few rows")
+    bt = Batch(23, G, D, 2, [700, 130, 64, 0], [T, max(1, T // 2)], q_scale=6.0, few=few)
+    bt.q.copy_(bt.q.abs())
+    for i, n in enumerate(bt.lens):
+        rows = torch.from_numpy(sp.head_rows(bt.ids, bt.off, i, int(n))).cuda()
+        t = torch.arange(int(n), device="cuda")
+        size = 0.05 + 4.0 * (t / max(1, int(n) - 1) if rising else (t == 0))
+        k = bt.dev["kp"].view(-1, D)
+        k[rows] = (k[rows].float().abs() * size[:, None]).bfloat16()
+    bt.k.copy_(bt.k.abs() * 5)
+    bt.run()
+    bt.check()
+
+
 def test_two_tiles_split():
     bt = Batch(7, 4, 128, 1, [900], [64], workers=9)
     assert tg.tg_tree_plan_items(bt.plan)["n_merge"] == 1
@@ -125,24 +168,26 @@ def test_two_tiles_split():
     bt.check()
 
 
-@pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("T", [5, 40])
-def test_softcap(D, T):
-    bt = Batch(8, 4, D, 2, [100, 33, 0, 17], [T, 3], max_draft=T, q_scale=12.0)
+@pytest.mark.parametrize("D,T,few", [(64, 5, False), (64, 40, False), (128, 5, False), (128, 40, False), (128, 3, True),
+                                     (128, 8, True)])
+def test_softcap(D, T, few):
+    bt = Batch(8, 4, D, 2, [100, 33, 0, 17], [T, 3], max_draft=T, q_scale=12.0, few=few)
     bt.run(softcap=15.0)
     bt.check(softcap=15.0)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.05, 0.5])
-def test_scales(scale):
-    bt = Batch(9, 2, 128, 2, [50, 20, 129, 3], [5, 9])
+@pytest.mark.parametrize("few", [False, True])
+def test_scales(scale, few):
+    bt = Batch(9, 2, 128, 2, [50, 20, 129, 3], [5, 9], few=few)
     bt.run(scale=scale)
     bt.check(scale=scale)
 
 
-def test_stale_rows_and_foreign_drafts_do_not_leak():
+@pytest.mark.parametrize("few", [False, True])
+def test_stale_rows_and_foreign_drafts_do_not_leak(few):
     """NaN in every pool row that is not retained, in K and V; NaN behind the last sequence."""
-    bt = Batch(10, 4, 128, 2, [1, 17, 63, 66, 0, 129], [3, 9, 1], stale=float("nan"), extra_rows=4, cap_extra=40)
+    bt = Batch(10, 4, 128, 2, [1, 17, 63, 66, 0, 129], [3, 8, 1], stale=float("nan"), extra_rows=4, cap_extra=40, few=few)
     n = int(bt.doff[-1])
     for x in (bt.k, bt.v, bt.q):
         x[n:] = float("nan")
@@ -150,14 +195,15 @@ def test_stale_rows_and_foreign_drafts_do_not_leak():
     bt.check()
 
 
-@pytest.mark.parametrize("D,G,T", [(128, 4, 9), (64, 1, 40), (128, 8, 33)])
+@pytest.mark.parametrize("D,G,T,few", [(128, 4, 9, False), (64, 1, 40, False), (128, 8, 33, False), (128, 4, 8, True),
+                                       (128, 1, 13, True)])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
-def test_masked_drafted_values_do_not_leak(D, G, T, value):
+def test_masked_drafted_values_do_not_leak(D, G, T, few, value):
     """A drafted token whose K and V hold NaN or an infinity: the tokens that do not attend to it are
     as without it; those that do hold what 64 bits give in V's places."""
     masks = [1 << j for j in range(T)]
     masks = [m | (2 if j in (3, T - 1) else 0) for j, m in enumerate(masks)]   # token 1's other readers
-    bt = Batch(11, G, D, 1, [37], [T], masks=masks)
+    bt = Batch(11, G, D, 1, [37], [T], masks=masks, few=few)
     bt.v[1, 0, 5] = value
     bt.v[1, 0, D - 1] = value
     bt.run()
@@ -180,17 +226,20 @@ def test_masked_drafted_values_do_not_leak(D, G, T, value):
     assert torch.equal(o[others], clean[others])
 
 
-def test_rows_that_see_nothing():
+@pytest.mark.parametrize("few", [False, True])
+def test_rows_that_see_nothing(few):
     """No cache and an empty mask: out 0, lse -inf; mask bits past the draft are ignored."""
-    bt = Batch(12, 4, 128, 2, [0, 20, 0, 0], [4, 3], masks=[0, 2, 0xF0, 3, 2**64 - 1, 0, 0xFFF8])
+    bt = Batch(12, 4, 128, 2, [0, 20, 0, 0], [4, 3], masks=[0, 2, 0xF0, 3, 2**64 - 1, 0, 0xFFF8], few=few)
     bt.run()
     bt.check()
     assert bool(torch.isinf(bt.lse[0, :4]).all()) and bool(torch.isfinite(bt.lse[0, 4:]).all())
 
 
-def test_growing_heads_use_one_plan():
+@pytest.mark.parametrize("T", [5, 20])
+def test_growing_heads_use_one_plan(T):
     """Reserved pages that hold nothing yet are skipped, also as whole parts of a split head."""
-    bt = Batch(13, 4, 128, 2, [40, 0, 3, 500], [2, 5], cap_extra=900, workers=60)
+    bt = Batch(13, 4, 128, 2, [40, 0, 3, 500], [2, T], cap_extra=1900, workers=60)
+    assert bt.rows == (32 if T == 5 else 128)
     for n in ([40, 0, 3, 500], [0, 0, 0, 0], [41, 900, 17, 1400]):
         bt.lens = np.asarray(n, np.int64)
         bt.dev["n"].copy_(torch.tensor(n, dtype=torch.int32))
@@ -246,8 +295,9 @@ def test_other_stream_and_graph_replay():
     bt.check()
 
 
-def test_two_plans_on_two_streams():
-    bts = [Batch(18 + i, 4, 128, 2, [900, 40, 3, 260], [7, 12], workers=30) for i in range(2)]
+@pytest.mark.parametrize("few", [False, True])
+def test_two_plans_on_two_streams(few):
+    bts = [Batch(18 + i, 4, 128, 2, [900, 40, 3, 260], [7, 8], workers=30, few=few) for i in range(2)]
     torch.cuda.synchronize()
     ss = [torch.cuda.Stream() for _ in bts]
     for _ in range(5):
@@ -258,8 +308,13 @@ def test_two_plans_on_two_streams():
         bt.check()
 
 
-def test_repeats_are_bit_equal():
-    bt = Batch(20, 4, 128, 2, [900, 40, 3, 1260], [7, 12], workers=50)
+@pytest.mark.parametrize("few", [False, True])
+def test_repeats_are_bit_equal(few):
+    """Dynamic items go to whichever worker comes first; the results do not depend on it."""
+    rng = np.random.default_rng(1)
+    bt = Batch(20, 4, 128, 2, rng.integers(0, 2000, size=40), [7, 8, 3, 1] * 5, workers=20, few=few)
+    info = tg.tg_tree_plan_items(bt.plan)
+    assert info["worker_off"][-1] < info["n_items"]
     bt.run()
     torch.cuda.synchronize()
     o, l = bt.out.clone(), bt.lse.clone()
@@ -269,11 +324,12 @@ def test_repeats_are_bit_equal():
     assert torch.equal(o, bt.out) and torch.equal(l, bt.lse)
 
 
-def test_device_side_refusals():
+@pytest.mark.parametrize("few", [False, True])
+def test_device_side_refusals(few):
     """A page outside the pool, a length above the reserved one, a row outside its table and a draft
     wider than the plan are reported and skipped; the other sequences are right."""
     def case(change):
-        bt = Batch(21, 4, 128, 2, [100, 40, 3, 260], [7, 12])
+        bt = Batch(21, 4, 128, 2, [100, 40, 3, 260], [7, 8], few=few)
         change(bt)
         bt.run()
         torch.cuda.synchronize()
@@ -296,10 +352,10 @@ def test_device_side_refusals():
         bt.dev["n"][2] = -1
 
     def bad_row(bt):
-        bt.dev["off"][3] += 1
+        bt.dev["off"][3] = bt.ids.size   # past the table
 
     def wide(bt):
-        bt.dev["doff"][2] += 1
+        bt.dev["doff"][2:] += 1   # sequence 1 drafts one token more than the plan allows
 
     for change in (bad_page, negative_page, too_long, negative, bad_row, wide):
         case(change)

@@ -170,6 +170,13 @@ def _plan(cap, Hq, Hkv, T, D=128, workers=0, pages=1 << 20, **kw):
                                   num_workers=workers, host_only=True, **kw)
 
 
+@pytest.mark.parametrize("Hq,T,tokens,D,rows", [(8, 4, 4000, 128, 16), (8, 5, 4000, 128, 32), (8, 8, 4000, 128, 32),
+                                                (8, 9, 4000, 128, 128), (8, 8, 1000, 128, 128), (8, 4, 1000, 128, 16),
+                                                (8, 4, 200, 128, 128), (8, 4, 4000, 64, 128), (8, 33, 4000, 128, 256)])
+def test_plan_kernel_by_rows_and_lengths(Hq, T, tokens, D, rows):
+    assert tg.tg_tree_plan_items(_plan([tokens] * 4, Hq, 2, T, D=D))["rows"] == rows
+
+
 @pytest.mark.parametrize("seed", range(12))
 def test_plan_covers_every_page_once(seed):
     rng = np.random.default_rng(seed)
@@ -200,18 +207,19 @@ def test_plan_covers_every_page_once(seed):
     assert sorted(slots) == list(range(len(slots)))
 
 
-def test_plan_shares_are_even():
+@pytest.mark.parametrize("T,workers", [(16, 296), (5, 148)])
+def test_plan_shares_are_even(T, workers):
     rng = np.random.default_rng(0)
     cap = rng.integers(500, 8000, size=512)
-    info = tg.tg_tree_plan_items(_plan(cap, 32, 8, 16))
+    info = tg.tg_tree_plan_items(_plan(cap, 32, 8, T))
     it, off = info["items"], info["worker_off"]
     load = [int((it[a:b, 2] - it[a:b, 1]).sum()) for a, b in zip(off[:-1], off[1:])]
-    assert info["n_workers"] == 296 and max(load) <= 1.12 * np.mean(load)
+    assert info["n_workers"] == workers and max(load) <= 1.2 * np.mean(load)
     dyn = it[off[-1]:]
     left = (dyn[:, 2] - dyn[:, 1]).sum() / (it[:, 2] - it[:, 1]).sum()
-    assert 0.02 < left < 0.1                              # the rest is taken by ticket
+    assert 0.02 < left < 0.13                             # the rest is taken by ticket
     size = dyn[:, 2] - dyn[:, 1]
-    assert size.max() <= 64                               # in small items
+    assert size.max() <= 80                               # in small items
     small = tg.tg_tree_plan_items(_plan([500] * 8, 8, 8, 4))
     assert small["worker_off"][-1] == small["n_items"]    # a small step is all static
 
@@ -279,7 +287,7 @@ def test_device_calls_refuse_bad_arguments_on_the_host():
     assert lib.tg_tree_decode(plan.handle, 1, one, one, 1024, one, 256, one, 256, one, one, one, one, one, one, 1.0, 0.0,
                               one, one, None) == 1
     assert lib.tg_tree_plan_status(plan.handle, None) == 1
-    assert lib.tg_tree_plan_items(None, None, None, None, None, None, None) == 1
+    assert lib.tg_tree_plan_items(None, None, None, None, None, None, None, None) == 1
     lib.tg_tree_plan_destroy(None)
 
 
