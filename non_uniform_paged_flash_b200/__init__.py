@@ -247,7 +247,7 @@ def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 # ------------------------------------------------------------------------------------------
@@ -853,8 +853,8 @@ def _current():
     """The current CUDA device (these calls launch there); -2, no tensor's device, without one."""
     import torch
     try:
-        return torch.cuda.current_device()
-    except (RuntimeError, AssertionError):
+        return torch._C._cuda_getDevice()
+    except (RuntimeError, AssertionError, AttributeError):
         return -2
 
 

@@ -385,14 +385,20 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
                      ::"r"(smem_addr(const_cast<uint32_t *>(tmem_slot))), "r"(TL::kCols) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // the plan's own lists do not change between calls: read before the preceding kernel is done
+    // the plan's own lists do not change between calls: read before the preceding kernel is done (and
+    // what they point to is brought near; it is read after)
     int32_t i0 = 0, i1 = 0, n_static = 0;
     TreeItem first{};
     if (warp == 5 * TILES) {
         i0 = a.worker_off[blockIdx.x];
         i1 = a.worker_off[blockIdx.x + 1];
         n_static = a.worker_off[gridDim.x];
-        if (i0 < i1) first = a.items[i0];
+        if (i0 < i1) {
+            first = a.items[i0];
+            prefetch_l2(a.kv_len + first.bh);
+            prefetch_l2(a.head_off + first.bh);
+            prefetch_l2(a.draft_off + first.bh / a.Hkv);
+        }
     }
     fence_before();
     __syncthreads();
@@ -939,14 +945,20 @@ __global__ void __launch_bounds__(NarrowLayout<NR>::kThreads, 1)
                      ::"r"(smem_addr(const_cast<uint32_t *>(tmem_slot))), "r"(512u) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    // the plan's own lists do not change between calls: read before the preceding kernel is done
+    // the plan's own lists do not change between calls: read before the preceding kernel is done (and
+    // what they point to is brought near; it is read after)
     int32_t i0 = 0, i1 = 0, n_static = 0;
     TreeItem first{};
     if (warp == 9) {
         i0 = a.worker_off[blockIdx.x];
         i1 = a.worker_off[blockIdx.x + 1];
         n_static = a.worker_off[gridDim.x];
-        if (i0 < i1) first = a.items[i0];
+        if (i0 < i1) {
+            first = a.items[i0];
+            prefetch_l2(a.kv_len + first.bh);
+            prefetch_l2(a.head_off + first.bh);
+            prefetch_l2(a.draft_off + first.bh / a.Hkv);
+        }
     }
     fence_before();
     __syncthreads();
@@ -1665,12 +1677,13 @@ int token_map(CUtensorMap *tm, const void *base, int32_t D, int32_t heads, int64
 
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Pages' worth of an item's fixed work (draft block, Q, joining, output): the wide kernel's and the
-// narrow one's, and the shares of the cost laid out ahead of time. Measured per item on the serving
-// layer: 3 us and 4.5 us, against 0.4 us and 0.18 us a page.
-constexpr int kItemCost = 12, kItemCostNarrow = 24;
-constexpr int kMinShare = 16;  // no worker's share below this many pages' worth
-constexpr int kStaticPermille = 950, kStaticPermilleNarrow = 900;
+// Pages' worth of an item's fixed work (draft block, Q, joining, output), the wide kernel's and the
+// narrow one's; and the shares of the cost laid out ahead of time. Swept on the GQA batch (wide, 677 MB:
+// 131 us at 14 pages and 98 %, 133.8 at 12 and 95 %, 137 at 12 and 92 %) and the serving layer (narrow,
+// 5.1 GB: 784 us at 20 to 30 pages and 90 %, 810 at 20 and 95 %, 1004 at 20 and 100 %).
+constexpr int kItemCost = 14, kItemCostNarrow = 24;
+constexpr int kMinShare = 4;    // pages of a worker in a step too small to fill the machine
+constexpr int kStaticPermille = 980, kStaticPermilleNarrow = 900;
 
 // Work list. A unit is a (head, row block): a run of pages plus a fixed cost. Units are taken longest
 // first; the first kStaticPermille of the cost is laid end to end and cut into equal shares, one per
@@ -1685,16 +1698,20 @@ void build_items(tg_tree_plan *p, const int32_t *cap, int32_t num_workers) {
     std::vector<int32_t> order(static_cast<size_t>(BH));
     for (int64_t i = 0; i < BH; ++i) order[static_cast<size_t>(i)] = static_cast<int32_t>(i);
     std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return cap[x] > cap[y]; });
+    // A step that leaves workers without kMinShare pages is bound by latency: items cost nothing extra
+    // there, every head goes to as many workers as it has shares, and nothing is left for tickets.
     int64_t total = 0;
-    const int32_t item_cost = p->narrow ? kItemCostNarrow : kItemCost;
-    for (int64_t i = 0; i < BH; ++i) total += (cap[i] + 15) / 16 + item_cost;
+    for (int64_t i = 0; i < BH; ++i) total += (cap[i] + 15) / 16;
     total *= rblocks;
-    const int64_t nw = std::max<int64_t>(1, std::min<int64_t>(num_workers, total / kMinShare));
-    const int64_t fixed = nw == num_workers && nw > 1 && p->tiles == 1
+    const bool small = total < static_cast<int64_t>(num_workers) * kMinShare;
+    const int32_t item_cost = small ? 0 : p->narrow ? kItemCostNarrow : kItemCost;
+    total += BH * rblocks * item_cost;
+    const int64_t nw = std::max<int64_t>(1, small ? std::min<int64_t>(num_workers, std::max<int64_t>(total / kMinShare, BH * rblocks)) : num_workers);
+    const int64_t fixed = !small && nw > 1 && p->tiles == 1
                               ? total * (p->narrow ? kStaticPermilleNarrow : kStaticPermille) / 1000
                               : total;
     const int32_t cut = p->narrow ? kNPages : kCutPages;  // heads are cut at whole blocks
-    const int64_t min_dyn = p->narrow ? 32 : std::max<int64_t>(16, p->rows_item / 4 / cut * cut);
+    const int64_t min_dyn = p->narrow ? 32 : std::max<int64_t>(24, p->rows_item / 4 / cut * cut);
     p->worker_off.assign(1, 0);
     int64_t done = 0;  // cost laid out so far
     int64_t w = 1;     // the current worker's share ends at fixed * w / nw
@@ -1707,7 +1724,7 @@ void build_items(tg_tree_plan *p, const int32_t *cap, int32_t num_workers) {
             for (;;) {
                 int64_t room;  // pages this item may take
                 // the share is full when what is left of it would hold less than a block
-                while (w <= nw && done + (at == 0 ? item_cost : 0) + cut > fixed * w / nw) {
+                while (w <= nw && done + (at == 0 ? item_cost : 0) + std::min(cut, pages - at) > fixed * w / nw) {
                     if (w == nw && fixed == total) break;  // all static: the last worker takes the rest
                     p->worker_off.push_back(static_cast<int32_t>(p->items.size()));
                     ++w;
