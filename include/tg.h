@@ -714,7 +714,8 @@ int tg_tree_masks(int32_t B, const int32_t *draft_off, const int32_t *parent, ui
  * device -1 = current. wait_limit_us bounds any single wait in the kernel (0 = 4 s).
  * Owns one device allocation (work list, partial results of split heads, error word), made here;
  * calls on one plan share it, so they must be ordered (one stream, or events between).
- * Serves page = 16, D 64 or 128, G 1, 2, 4 or 8, pools below 2^27 pages (TG_EUNSUPPORTED otherwise).
+ * Serves page = 16, D 64 or 128, G 1, 2, 4 or 8, pools below 2^27 pages, up to 65536 workers
+ * (TG_EUNSUPPORTED otherwise).
  * TG_EINVAL for other bad arguments; TG_ENOMEM; *out is NULL on error. */
 typedef struct tg_tree_plan tg_tree_plan;
 int tg_tree_plan_create(const tg_shape *shape, const int32_t *kv_cap, int32_t max_draft,
@@ -730,7 +731,8 @@ void tg_tree_plan_destroy(tg_tree_plan *p);
 int tg_tree_plan_items(const tg_tree_plan *p, int32_t *n_items, int32_t *n_workers,
                        int32_t *n_merge, int32_t *rows, int64_t *device_bytes, int32_t *items,
                        int32_t *worker_off);
-/* As tg_plan_status, for the calls on a tree plan. */
+/* As tg_plan_status, for the calls on a tree plan (TG_EBADPAGE also for drafts and lengths that do not
+ * fit the plan). */
 int tg_tree_plan_status(tg_tree_plan *p, tg_stream stream);
 
 /* Attention of the drafted tokens over the ragged paged cache and over each other. For drafted
@@ -747,7 +749,8 @@ int tg_tree_plan_status(tg_tree_plan *p, tg_stream stream);
  *   out bf16 [n_tokens][Hq][D] and lse fp32 [n_tokens][Hq], contiguous; rows behind the last
  *   sequence are left as they were. n_tokens: rows of these arrays, >= draft_off[B].
  * A drafted token alone (mask bit 0) is a decode step whose token is not in the cache yet.
- * bf16 products, fp32 accumulation, P rounded to bf16; deterministic. One kernel, and a merge
+ * scale and softcap must be finite, softcap >= 0 (TG_EINVAL); page_table may be NULL when no head
+ * reserves a page. bf16 products, fp32 accumulation, P rounded to bf16; deterministic. One kernel, and a merge
  * kernel (programmatic dependent) when the plan splits heads. Sequences whose draft does not fit
  * the plan or n_tokens, and lengths above the reserved ones, are skipped (TG_EBADPAGE through
  * tg_tree_plan_status; their rows are unspecified), as are bad page ids and rows. */

@@ -50,6 +50,7 @@ struct tg_tree_plan {
     tg_shape shape{};
     int32_t G = 0, max_draft = 0, tiles = 1;
     bool host_only = true;
+    bool any_pages = false;  // some head reserves a page
     int device = 0;
     uint64_t wait_ns = 4000000000ull;
     int32_t n_workers = 0;
@@ -865,7 +866,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
 // ------------------------------------------------------------------------------------------
 constexpr int kNBlock = 128;           // tokens of a block
 constexpr int kNPages = 8;
-constexpr float kNarrowSlack = 40.f;   // 2^40 times 2^30 tokens times |v| stays in fp32
+constexpr float kNarrowSlack = 20.f;   // sums of 2^30 tokens' 2^20 |v| stay in fp32 up to |v| = 2^77
 constexpr float kNoScore = -1e30f;     // base of a row that has seen no score
 
 template <int NR>
@@ -1888,10 +1889,14 @@ int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft
         max_draft > TG_MAX_DRAFT || BH * 8 > INT32_MAX || s->num_pages > (INT32_MAX / 16))
         return TG_EUNSUPPORTED;
     if (BH > 0 && !kv_cap) return TG_EINVAL;
+    int64_t pages = 0;
     for (int64_t i = 0; i < BH; ++i) {
         if (kv_cap[i] < 0) return TG_EINVAL;
         if (kv_cap[i] > TG_MAX_HEAD_TOKENS) return TG_EUNSUPPORTED;
+        pages += (kv_cap[i] + 15) / 16;
     }
+    // costs times workers stay in 64 bits
+    if (pages > (1ll << 40) || num_workers > 65536) return TG_EUNSUPPORTED;
     for (int32_t g = 0; g < n_groups; ++g)
         if (group_off[g] < 0 || group_off[g + 1] < group_off[g]) return TG_EINVAL;
     for (int32_t h = 0; h < s->Hkv; ++h)
@@ -1911,8 +1916,6 @@ int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft
     // 4 to 16 rows:  8: 104 : 87   23: 124 : 131   45: 175 : 184   90: 144 : 146   180: 259 : 314
     // 32 rows:       8: 125 : 97   23: 168 : 151   45: 232 : 208   90: 174 : 170   180: 286 : 308
     // (64 rows of a variant with NR = 64: 180: 199 : 134, its softmax no longer hidden by the loads.)
-    int64_t pages = 0;
-    for (int64_t i = 0; i < BH; ++i) pages += (kv_cap[i] + 15) / 16;
     const int32_t rows = max_draft * G;
     if (s->D == 128 && rows <= 32 && pages >= BH * (rows <= 16 ? 16 : 112)) {
         p->narrow = rows <= 16 ? 16 : 32;
@@ -1923,6 +1926,7 @@ int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft
     else
         p->tiles == 1 ? set_geometry<64, 1>(p.get()) : set_geometry<64, 2>(p.get());
     p->host_only = host_only != 0;
+    p->any_pages = pages > 0;
     if (wait_limit_us > 0) p->wait_ns = static_cast<uint64_t>(wait_limit_us) * 1000ull;
     for (int32_t h = 0; h < s->Hkv; ++h) {
         p->row_lo.push_back(group_off[group_of_head[h]]);
@@ -2038,7 +2042,11 @@ extern "C" int tg_tree_plan_status(tg_tree_plan *p, tg_stream stream) {
     TG_TRY(cudaMemcpyAsync(&err, p->d_err, 4, cudaMemcpyDeviceToHost, st));
     TG_TRY(cudaMemsetAsync(p->d_err, 0, 4, st));
     TG_TRY(cudaStreamSynchronize(st));
-    if (err & kErrTimeout) return TG_ETIMEOUT;
+    if (err & kErrTimeout) {  // a stopped call may have left its tickets part-counted
+        TG_TRY(cudaMemsetAsync(p->d_ticket, 0, 8, st));
+        TG_TRY(cudaStreamSynchronize(st));
+        return TG_ETIMEOUT;
+    }
     return err ? TG_EBADPAGE : TG_OK;
 }
 
@@ -2051,10 +2059,10 @@ extern "C" int tg_tree_decode(tg_tree_plan *p, int64_t n_tokens, const int32_t *
     const tg_shape &s = p->shape;
     if (s.B == 0 || n_tokens == 0) return TG_OK;
     const int64_t qw = static_cast<int64_t>(s.Hq) * s.D, kw = static_cast<int64_t>(s.Hkv) * s.D;
-    if (!draft_off || !q || !k_draft || !v_draft || !tree_mask || !page_table || !head_page_off || !head_kv_len || !out ||
+    if (!draft_off || !q || !k_draft || !v_draft || !tree_mask || (p->any_pages && !page_table) || !head_page_off || !head_kv_len || !out ||
         !lse || !al16(q) || !al16(k_draft) || !al16(v_draft) || !al16(k_pages) || !al16(v_pages) || !al16(out) ||
         q_stride < qw || k_stride < kw || v_stride < kw || q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0 ||
-        !(scale == scale) || !(softcap >= 0.f) || (s.num_pages > 0 && (!k_pages || !v_pages)))
+        !std::isfinite(scale) || !std::isfinite(softcap) || softcap < 0.f || (s.num_pages > 0 && (!k_pages || !v_pages)))
         return TG_EINVAL;
     int cur = 0;
     TG_TRY(cudaGetDevice(&cur));
@@ -2095,6 +2103,8 @@ extern "C" int tg_tree_decode(tg_tree_plan *p, int64_t n_tokens, const int32_t *
         double k = static_cast<double>(scale) / softcap;
         for (int i = 0; i < 4; ++i, k *= (static_cast<double>(scale) / softcap) * (static_cast<double>(scale) / softcap))
             a.cap_p[i] = static_cast<float>(static_cast<double>(softcap) * 1.4426950408889634 * kTanh[i] * k);
+        for (float c : a.cap_p)
+            if (!std::isfinite(c)) a.cap_x = INFINITY;  // a tiny cap: the general form for all scores
     }
     a.v_draft = static_cast<const __nv_bfloat16 *>(v_draft);
     a.v_stride = v_stride;

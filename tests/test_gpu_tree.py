@@ -259,11 +259,21 @@ def test_no_drafts_and_no_sequences():
                       torch.zeros(0, device="cuda"))
 
 
-def test_no_pages_at_all():
-    """Heads without any reserved token attend to the draft alone."""
-    bt = Batch(15, 2, 64, 2, [0, 0], [5])
+@pytest.mark.parametrize("D", [64, 128])
+def test_no_pages_at_all(D):
+    """Heads without any reserved token attend to the draft alone; there is no table then."""
+    bt = Batch(15, 2, D, 2, [0, 0], [5])
+    bt.dev["table"] = torch.zeros(0, dtype=torch.int32, device="cuda")
     bt.run()
     bt.check()
+
+
+@pytest.mark.parametrize("softcap", [1e-9, 1e-3, 1e9])
+@pytest.mark.parametrize("few", [False, True])
+def test_extreme_caps(softcap, few):
+    bt = Batch(24, 4, 128, 2, [100, 33, 0, 17], [5, 3], few=few)
+    bt.run(softcap=softcap)
+    bt.check(softcap=softcap)
 
 
 def test_contiguous_inputs_give_the_same_bits():
@@ -373,7 +383,8 @@ def test_argument_refusals():
                       ("head_page_off", d["off"].int()), ("out", bt.out.transpose(0, 1))):
         with pytest.raises(ValueError):
             tg.tg_tree_decode(**{**good, name: bad})
-    for kw in (dict(softcap=-1.0), dict(softcap=float("nan")), dict(scale=float("nan"))):
+    for kw in (dict(softcap=-1.0), dict(softcap=float("nan")), dict(scale=float("nan")), dict(scale=float("inf")),
+               dict(softcap=float("inf"))):
         with pytest.raises(tg.TGError) as e:
             tg.tg_tree_decode(**{**good, **kw})
         assert e.value.status == tg.TG_EINVAL

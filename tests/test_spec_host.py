@@ -228,7 +228,7 @@ def test_plan_shares_are_even(T, workers):
     (dict(T=0), tg.TG_EINVAL), (dict(T=65), tg.TG_EUNSUPPORTED), (dict(D=96), tg.TG_EUNSUPPORTED),
     (dict(Hq=6), tg.TG_EUNSUPPORTED), (dict(Hq=7), tg.TG_EINVAL), (dict(cap=[-1, 0]), tg.TG_EINVAL),
     (dict(cap=[tg.TG_MAX_HEAD_TOKENS + 1, 0]), tg.TG_EUNSUPPORTED), (dict(pages=1 << 28), tg.TG_EUNSUPPORTED),
-    (dict(pages=-1), tg.TG_EINVAL), (dict(workers=-1), tg.TG_EINVAL), (dict(device=-2), tg.TG_EINVAL),
+    (dict(pages=-1), tg.TG_EINVAL), (dict(workers=-1), tg.TG_EINVAL), (dict(workers=65537), tg.TG_EUNSUPPORTED), (dict(device=-2), tg.TG_EINVAL),
     (dict(wait_limit_us=-1), tg.TG_EINVAL)])
 def test_plan_refusals(kw, status):
     args = dict(cap=[30, 40], Hq=8, Hkv=2, T=4)
