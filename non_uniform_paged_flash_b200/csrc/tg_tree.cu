@@ -112,8 +112,9 @@ struct TreeLayout {
     static constexpr int kHalves = D / 64;             // 128-byte column halves
     static constexpr int kEntry = kBlock * D * 2;      // K or V of a block
     static constexpr int kGroup = 1024 * kHalves;      // 8 tokens of it: a swizzled atom per half
-    // full[E], empty[E], q_full[2], q_empty[2], per tile: s_full[2], p_full[2], o_done[2], drain
-    static constexpr int kControl = kHdr * static_cast<int>(sizeof(BlockHdr)) + 8 * (2 * kMaxEntries + 4 + 7 * TILES) + 16;
+    // full[E], empty[E], q_full[2], q_empty[2], per tile: s_full[2], p_full[2], o_done[2], drain, and with
+    // two tiles turn[4]
+    static constexpr int kControl = kHdr * static_cast<int>(sizeof(BlockHdr)) + 8 * (2 * kMaxEntries + 4 + (TILES == 1 ? 7 : 11) * TILES) + 16;
     // one CTA of two tiles, or two CTAs of one tile, per SM (228 KB, 1 KB of it reserved per CTA)
     static constexpr int kLimit = TILES == 1 ? (228 * 1024) / 2 - 1024 : 227 * 1024;
     static constexpr int kThreads = 32 * (5 * TILES + 1);
@@ -355,7 +356,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
     const uint32_t full = smem_addr(control) + kHdr * static_cast<uint32_t>(sizeof(BlockHdr));
     const uint32_t empty = full + 8 * kMaxEntries, q_full = empty + 8 * kMaxEntries, q_empty = q_full + 16;
     const uint32_t s_full = q_empty + 16, p_full = s_full + 16 * TILES, o_done = p_full + 16 * TILES,
-                   drain = o_done + 16 * TILES;
+                   drain = o_done + 16 * TILES, turn = drain + 8 * TILES;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(control + TL::kControl - 16);
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -378,6 +379,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
             mbar_init(o_done + 8 * k, 1);
         }
         for (int t = 0; t < TILES; ++t) mbar_init(drain + 8 * t, 1);
+        for (int t = 0; TILES > 1 && t < 4 * TILES; ++t) mbar_init(turn + 8 * t, 1);
         *abort_flag = (sbase & 1023u) ? 1 : 0;  // swizzled tiles need 1024-byte alignment
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -655,6 +657,17 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
         float m = -INFINITY, le = 0.f;
         unsigned long long mask = 0ull;
         bool ok = *abort_flag == 0;
+        // With two tiles and capped scores, the two warps of a scheduler take turns at the exponentials, so
+        // that one's share of the special-function unit falls on the other's polynomials (64-token capped
+        // trees 293 -> 275 us; without a cap there is too little other work: 266 against 271 us).
+        constexpr bool TURNS = TILES > 1 && CAP;
+        auto my_turn = [&](int32_t blk) {
+            return !TURNS || mbar_wait(turn + 8 * (4 * t + qd), static_cast<uint32_t>(t == 0 ? blk + 1 : blk) & 1u, a.wait_ns, abort_flag);
+        };
+        auto pass_turn = [&]() {
+            __syncwarp();
+            if (TURNS && lane == 0) mbar_arrive(turn + 8 * (4 * (t ^ 1) + qd));
+        };
         for (int32_t blk = 0; ok; ++blk) {
             const int bf = blk & 1;
             ok = mbar_wait(s_full + 8 * (2 * t + bf), static_cast<uint32_t>(blk >> 1) & 1u, a.wait_ns, abort_flag);
@@ -667,6 +680,8 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
             const int32_t nv = (info >> 8) & 0xFF, nrow = info >> 16;
             const bool valid = i < nrow;
             if (w0 >= nrow) {  // no row of this warp
+                ok = my_turn(blk);
+                pass_turn();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_full + 8 * (2 * t + bf));
                 continue;
@@ -744,6 +759,10 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
             // for the sum; m stays -inf while nothing counted: p = 0 then
             const float nm = m == -INFINITY ? 0.f : -m;
             const f2 nm2 = pair(nm, nm), sc2 = pair(sl2, sl2);
+            if (TURNS) {
+                ok = my_turn(blk);
+                if (!__all_sync(FULL, ok)) { ok = false; break; }
+            }
             f2 ls[4] = {pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f), pair(0.f, 0.f)};
             uint32_t pw[32];
 #pragma unroll
@@ -755,6 +774,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
                 ls[e & 3] = add2(ls[e & 3], pair(p0, p1));
                 pw[e] = pack_bf16(p0, p1);
             }
+            pass_turn();
             tmem_st32(t_s + 64 * bf, pw);
             {
                 float u, w;
