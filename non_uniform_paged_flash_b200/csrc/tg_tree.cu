@@ -55,10 +55,8 @@ struct tg_tree_plan {
     uint64_t wait_ns = 4000000000ull;
     int32_t n_workers = 0;
     int32_t rows_item = 0;   // query rows of an item at most
-    int32_t q_rows = 0;      // rows of one Q box (multiple of 8)
+    int32_t q_rows = 0;      // query rows that an item's Q load brings, per tile
     int32_t narrow = 0;      // rows of the narrow kernel (16 or 32), 0: wide kernel
-    int32_t q_boxes = 1;     // Q boxes in shared memory
-    int32_t entries = 0;     // K / V ring entries
     int32_t smem_bytes = 0;
     int32_t n_slots = 0;
     std::vector<tg::TreeItem> items;      // each worker's items, then the dynamic ones
@@ -100,29 +98,32 @@ struct alignas(16) BlockHdr {
     int32_t h;      // KV head
     int32_t slot;   // partial-result slot or -1
     int32_t row0;   // first query row of the item
-    int16_t qb;     // the item's Q box
-    int16_t v_fill; // ring fill (modulo 2 entries) that brings the block's V
+    int32_t v_fill; // ring fill (modulo 2 entries) that brings the block's V
     unsigned long long bad;  // drafted tokens whose V row holds an infinity or NaN
 };
 static_assert(sizeof(BlockHdr) == 32, "BlockHdr layout");
 
-// Shared memory: Q boxes (q_rows query rows each, per tile), the K / V ring, block headers, barriers.
+// Shared memory: a Q tile of 128 rows per tile, the K / V ring, block headers, barriers. Rows that the plan's
+// drafts never use are zeros, so that they cost the products little power: the steps that the loads bound
+// run under the power cap, whose clock goes down with what the padding rows multiply.
 template <int D, int TILES>
 struct TreeLayout {
     static constexpr int kHalves = D / 64;             // 128-byte column halves
     static constexpr int kEntry = kBlock * D * 2;      // K or V of a block
     static constexpr int kGroup = 1024 * kHalves;      // 8 tokens of it: a swizzled atom per half
-    // full[E], empty[E], q_full[2], q_empty[2], per tile: s_full[2], p_full[2], o_done[2], drain, and with
+    // full[E], empty[E], q_full, q_empty, per tile: s_full[2], p_full[2], o_done[2], drain, and with
     // two tiles turn[4]
-    static constexpr int kControl = kHdr * static_cast<int>(sizeof(BlockHdr)) + 8 * (2 * kMaxEntries + 4 + (TILES == 1 ? 7 : 11) * TILES) + 16;
+    static constexpr int kControl = kHdr * static_cast<int>(sizeof(BlockHdr)) + 8 * (2 * kMaxEntries + 2 + (TILES == 1 ? 7 : 11) * TILES) + 16;
     // one CTA of two tiles, or two CTAs of one tile, per SM (228 KB, 1 KB of it reserved per CTA)
     static constexpr int kLimit = TILES == 1 ? (228 * 1024) / 2 - 1024 : 227 * 1024;
     static constexpr int kThreads = 32 * (5 * TILES + 1);
     static constexpr uint32_t kCols = 256u * TILES;    // tensor-memory columns
-    static int q_bytes(int q_rows, int boxes) { return (boxes * TILES * q_rows * D * 2 + 1023) / 1024 * 1024; }
-    static int entries(int q_rows, int boxes) {
-        return std::min(kMaxEntries, (kLimit - q_bytes(q_rows, boxes) - kControl) / kEntry);
-    }
+    static constexpr int kQTile = kRows * D * 2;
+    static constexpr int kEntries = (kLimit - TILES * kQTile - kControl) / kEntry < kMaxEntries
+                                        ? (kLimit - TILES * kQTile - kControl) / kEntry
+                                        : kMaxEntries;
+    static constexpr int kRing = TILES * kQTile;
+    static constexpr int kBytes = kRing + kEntries * kEntry + kControl;
 };
 
 struct TreeArgs {
@@ -130,7 +131,6 @@ struct TreeArgs {
     const int32_t *worker_off;
     int32_t n_items;
     int32_t G, g_shift, Hq, Hkv, max_draft, q_rows, rows_item;
-    int32_t q_boxes, entries, ring;  // ring: offset of the K / V ring in shared memory
     int64_t n_tokens, num_pages;
     float scale_log2;       // scale * log2 e
     float cap2;             // softcap * log2 e
@@ -349,30 +349,32 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
     constexpr int KS = D / 16;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = smem_addr(smem);
-    const int NE = a.entries;
-    const uint32_t ring = sbase + a.ring;
-    unsigned char *control = smem + a.ring + NE * TL::kEntry;
+    constexpr int NE = TL::kEntries;
+    const uint32_t ring = sbase + TL::kRing;
+    unsigned char *control = smem + TL::kRing + NE * TL::kEntry;
     BlockHdr *hdrs = reinterpret_cast<BlockHdr *>(control);
     const uint32_t full = smem_addr(control) + kHdr * static_cast<uint32_t>(sizeof(BlockHdr));
-    const uint32_t empty = full + 8 * kMaxEntries, q_full = empty + 8 * kMaxEntries, q_empty = q_full + 16;
-    const uint32_t s_full = q_empty + 16, p_full = s_full + 16 * TILES, o_done = p_full + 16 * TILES,
+    const uint32_t empty = full + 8 * kMaxEntries, q_full = empty + 8 * kMaxEntries, q_empty = q_full + 8;
+    const uint32_t s_full = q_empty + 8, p_full = s_full + 16 * TILES, o_done = p_full + 16 * TILES,
                    drain = o_done + 16 * TILES, turn = drain + 8 * TILES;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(control + TL::kControl - 16);
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int nq = a.q_boxes;
-    const uint32_t q_half = static_cast<uint32_t>(a.q_rows) * 128u;  // bytes of one column half of a box
-    const uint32_t q_tile = q_half * TL::kHalves;                    // one tile's part of a box
+    constexpr uint32_t q_half = kRows * 128u;  // bytes of one column half of a Q tile
 
+    // the Q rows that no draft of the plan fills
+    for (int c = threadIdx.x; c < (kRows - a.q_rows) * 8 * TL::kHalves; c += TL::kThreads) {
+        const int hf = c / ((kRows - a.q_rows) * 8), r = c - hf * ((kRows - a.q_rows) * 8);
+        *reinterpret_cast<uint4 *>(smem + hf * q_half + a.q_rows * 128 + r * 16) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    ptx::fence_async_smem();
     if (threadIdx.x == 0) {
         for (int e = 0; e < NE; ++e) {
             mbar_init(full + 8 * e, 1);
             mbar_init(empty + 8 * e, TILES);
         }
-        for (int k = 0; k < 2; ++k) {
-            mbar_init(q_full + 8 * k, 1);
-            mbar_init(q_empty + 8 * k, TILES);
-        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, TILES);
         for (int k = 0; k < 2 * TILES; ++k) {
             mbar_init(s_full + 8 * k, 1);
             mbar_init(p_full + 8 * k, 4);
@@ -443,7 +445,6 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
             const int32_t *row = a.table + s.off + s.it.page_begin;
             int32_t ids = lane < np ? __ldg(row + lane) : -1;
             int32_t ids_next = 32 + lane < np ? __ldg(row + 32 + lane) : -1;
-            const int qb = nq == 2 ? (qn & 1) : 0;
             // Fills go in the order of use: K(0), then K(j) and V(j - 1), then V of the last block.
             int32_t pid = 0, p_pid = 0, boxes = 0, p_boxes = 0;
             bool is_draft = false, p_draft = false;
@@ -497,26 +498,25 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
                     hd->h = h;
                     hd->slot = s.it.slot;
                     hd->row0 = s.it.row0;
-                    hd->qb = static_cast<int16_t>(qb);
-                    hd->v_fill = static_cast<int16_t>((fills + 1 + (j > 0) + !last) % (2 * NE));
+                    hd->v_fill = (fills + 1 + (j > 0) + !last) % (2 * NE);
                     hd->bad = 0ull;
                 }
                 fill(false, is_draft, pid, boxes);
                 if (j == 0) {
-                    // the item's query rows, into a box whose last scores are done
+                    // the item's query rows, once the last item's scores are done
                     int32_t bad = 0;
                     if (lane == 0) {
-                        if (!mbar_wait(q_empty + 8 * qb, (static_cast<uint32_t>(qn / nq) & 1u) ^ 1u, a.wait_ns, abort_flag)) {
+                        if (!mbar_wait(q_empty, (static_cast<uint32_t>(qn) & 1u) ^ 1u, a.wait_ns, abort_flag)) {
                             timed_out();
                             bad = 1;
                         } else {
-                            mbar_expect_tx(q_full + 8 * qb, q_tile * TILES);
+                            mbar_expect_tx(q_full, static_cast<uint32_t>(a.q_rows) * D * 2u * TILES);
 #pragma unroll
                             for (int t = 0; t < TILES; ++t)
 #pragma unroll
                                 for (int qh = 0; qh < TL::kHalves; ++qh)
-                                    tma_3d(sbase + (qb * TILES + t) * q_tile + qh * q_half, &tm_q, qh * 64, h * a.G,
-                                           s.tok0 + ((s.it.row0 + t * kRows) >> a.g_shift), q_full + 8 * qb);
+                                    tma_3d(sbase + t * TL::kQTile + qh * q_half, &tm_q, qh * 64, h * a.G,
+                                           s.tok0 + ((s.it.row0 + t * kRows) >> a.g_shift), q_full);
                         }
                     }
                     if (__shfl_sync(FULL, bad, 0)) {
@@ -548,8 +548,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
             const uint64_t lim = a.wait_ns < kDrainNs ? a.wait_ns : kDrainNs;
             for (int32_t f = max(0, fills - NE + (ended ? 1 : 0)); f < fills; ++f)
                 mbar_wait(full + 8 * (f % NE), static_cast<uint32_t>(f / NE) & 1u, lim);
-            for (int32_t k = max(0, qn - nq); k < qn; ++k)
-                mbar_wait(q_full + 8 * (k % nq), static_cast<uint32_t>(k / nq) & 1u, lim);
+            if (qn > 0) mbar_wait(q_full, static_cast<uint32_t>(qn - 1) & 1u, lim);
             walk.finish();
         }
         __syncwarp();
@@ -565,7 +564,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
             constexpr uint32_t hi_q = sdesc_hi(1024), hi_kv = sdesc_hi(TL::kGroup);
             constexpr uint32_t id_s = idesc_bf16(kBlock, kRows, 0), id_o = idesc_bf16(D, kRows, 1);
             const uint32_t tm = tmem + 256 * t, t_o = tm + 128;
-            const uint32_t k_lo = sdesc_lo(ring, 16), v_lo = sdesc_lo(ring, 1024), q_lo = sdesc_lo(sbase, 16) + ((t * q_tile) >> 4);
+            const uint32_t k_lo = sdesc_lo(ring, 16), v_lo = sdesc_lo(ring, 1024), q_lo = sdesc_lo(sbase + t * TL::kQTile, 16);
             bool ok = *abort_flag == 0;
             int32_t qn = 0, ent = 0;  // the ring's entries come in the order of use
             uint32_t eph = 0u;
@@ -613,24 +612,24 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
                 const bool on = (info >> 16) > t * kRows;
                 if (!(info & kStop)) {
                     if (info & kFirst) {
-                        ok = mbar_wait(q_full + 8 * hd->qb, static_cast<uint32_t>(qn / nq) & 1u, a.wait_ns, abort_flag);
+                        ok = mbar_wait(q_full, static_cast<uint32_t>(qn) & 1u, a.wait_ns, abort_flag);
                         if (!ok) break;
                         ++qn;
                     }
                     fence_after();
                     if (on) {
-                        const uint32_t q = q_lo + ((hd->qb * TILES * q_tile) >> 4), k = k_lo + ent * (TL::kEntry >> 4);
+                        const uint32_t k = k_lo + ent * (TL::kEntry >> 4);
 #pragma unroll
                         for (int ks = 0; ks < KS; ++ks)
-                            mma_ss(tm + 64 * bf, q + (ks / 4) * (q_half >> 4) + (ks % 4) * 2, hi_q,
+                            mma_ss(tm + 64 * bf, q_lo + (ks / 4) * (q_half >> 4) + (ks % 4) * 2, hi_q,
                                    k + (ks / 4) * (1024 >> 4) + (ks % 4) * 2, hi_kv, id_s, ks > 0);
                         mma_commit(s_full + 8 * (2 * t + bf));
                         mma_commit(empty + 8 * ent);
-                        if (info & kLast) mma_commit(q_empty + 8 * hd->qb);
+                        if (info & kLast) mma_commit(q_empty);
                     } else {
                         mbar_arrive(s_full + 8 * (2 * t + bf));
                         mbar_arrive(empty + 8 * ent);
-                        if (info & kLast) mbar_arrive(q_empty + 8 * hd->qb);
+                        if (info & kLast) mbar_arrive(q_empty);
                     }
                 } else {
                     mbar_arrive(s_full + 8 * (2 * t + bf));
@@ -942,6 +941,9 @@ __global__ void __launch_bounds__(NarrowLayout<NR>::kThreads, 1)
     volatile unsigned long long *item_bad = reinterpret_cast<volatile unsigned long long *>(tail + 16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    // Q rows that no draft of the plan fills are zeros (see TreeLayout)
+    for (int c = threadIdx.x; c < NL::kQBoxes * NL::kQBox / 16; c += NL::kThreads) reinterpret_cast<uint4 *>(smem)[c] = make_uint4(0u, 0u, 0u, 0u);
+    fence_async_smem();
     if (threadIdx.x == 0) {
         for (int e = 0; e < NE; ++e) {
             mbar_init(full + 8 * e, 1);
@@ -1080,8 +1082,7 @@ __global__ void __launch_bounds__(NarrowLayout<NR>::kThreads, 1)
                     hd->h = sh.h;
                     hd->slot = s.it.slot;
                     hd->row0 = s.it.row0;
-                    hd->qb = static_cast<int16_t>(qb);
-                    hd->v_fill = static_cast<int16_t>((fill0 + (last ? 2 * nblk - 1 : j == nblk - 2 ? 2 * nblk - 2 : 2 * j + 3)) % (2 * NE));
+                    hd->v_fill = (fill0 + (last ? 2 * nblk - 1 : j == nblk - 2 ? 2 * nblk - 2 : 2 * j + 3)) % (2 * NE);
                     hd->bad = 0ull;
                 }
                 fill(false, is_draft, pid[0], boxes[0]);
@@ -1093,7 +1094,7 @@ __global__ void __launch_bounds__(NarrowLayout<NR>::kThreads, 1)
                             timed_out();
                             bad = 1;
                         } else {
-                            mbar_expect_tx(q_full + 8 * qb, NL::kQBox);
+                            mbar_expect_tx(q_full + 8 * qb, static_cast<uint32_t>(a.q_rows) * D * 2u);
 #pragma unroll
                             for (int qh = 0; qh < 2; ++qh)
                                 tma_3d(sbase + qb * NL::kQBox + qh * (NL::kQBox / 2), &tm_q, qh * 64, sh.h * a.G,
@@ -1791,7 +1792,7 @@ void build_items(tg_tree_plan *p, const int32_t *cap, int32_t num_workers) {
 template <int D, int TILES, bool CAP>
 int set_smem() {
     TG_TRY(cudaFuncSetAttribute(tree_kernel<D, TILES, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                TreeLayout<D, TILES>::kLimit));
+                                TreeLayout<D, TILES>::kBytes));
     return TG_OK;
 }
 template <int D, int TILES>
@@ -1887,14 +1888,6 @@ struct TreeFree {
     void operator()(tg_tree_plan *p) const { tree_free(p); }
 };
 
-template <int D, int TILES>
-void set_geometry(tg_tree_plan *p) {
-    using TL = TreeLayout<D, TILES>;
-    p->q_boxes = TL::entries(p->q_rows, 2) >= 5 ? 2 : 1;
-    p->entries = TL::entries(p->q_rows, p->q_boxes);
-    p->smem_bytes = TL::q_bytes(p->q_rows, p->q_boxes) + p->entries * TL::kEntry + TL::kControl;
-}
-
 int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft, const int32_t *group_of_head,
                      const int64_t *group_off, int32_t n_groups, int32_t num_workers, int32_t host_only, int32_t device,
                      int32_t wait_limit_us, tg_tree_plan **out) {
@@ -1928,9 +1921,7 @@ int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft
     p->max_draft = max_draft;
     p->tiles = max_draft * G > kRows ? 2 : 1;
     p->rows_item = p->tiles == 2 ? 2 * kRows : max_draft * G;
-    p->q_rows = p->tiles == 2 ? kRows : (max_draft * G + 7) / 8 * 8;
-    // a second Q box lets the next item's queries load beside the current one's, where it costs at
-    // most one ring entry
+    p->q_rows = p->tiles == 2 ? kRows : max_draft * G;
     // The narrow kernel, whose items cost more and whose tokens cost less, from the mean pages of a head
     // on at which it measured faster (256 or 128 sequences of 32/8 heads, us narrow : wide, by mean pages).
     // 4 to 16 rows:  8: 104 : 87   23: 124 : 131   45: 175 : 184   90: 144 : 146   180: 259 : 314
@@ -1939,12 +1930,12 @@ int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft
     const int32_t rows = max_draft * G;
     if (s->D == 128 && rows <= 32 && pages >= BH * (rows <= 16 ? 16 : 112)) {
         p->narrow = rows <= 16 ? 16 : 32;
-        p->q_rows = p->narrow;
         p->smem_bytes = p->narrow == 16 ? NarrowLayout<16>::kBytes : NarrowLayout<32>::kBytes;
-    } else if (s->D == 128)
-        p->tiles == 1 ? set_geometry<128, 1>(p.get()) : set_geometry<128, 2>(p.get());
-    else
-        p->tiles == 1 ? set_geometry<64, 1>(p.get()) : set_geometry<64, 2>(p.get());
+    } else if (s->D == 128) {
+        p->smem_bytes = p->tiles == 1 ? TreeLayout<128, 1>::kBytes : TreeLayout<128, 2>::kBytes;
+    } else {
+        p->smem_bytes = p->tiles == 1 ? TreeLayout<64, 1>::kBytes : TreeLayout<64, 2>::kBytes;
+    }
     p->host_only = host_only != 0;
     p->any_pages = pages > 0;
     if (wait_limit_us > 0) p->wait_ns = static_cast<uint64_t>(wait_limit_us) * 1000ull;
@@ -2102,9 +2093,6 @@ extern "C" int tg_tree_decode(tg_tree_plan *p, int64_t n_tokens, const int32_t *
     a.items = p->d_items;
     a.worker_off = p->d_worker_off;
     a.n_items = static_cast<int32_t>(p->items.size());
-    a.q_boxes = p->q_boxes;
-    a.entries = p->entries;
-    a.ring = (p->q_boxes * p->tiles * p->q_rows * s.D * 2 + 1023) / 1024 * 1024;
     a.ticket = p->d_ticket;
     a.G = p->G;
     a.g_shift = p->G == 1 ? 0 : p->G == 2 ? 1 : p->G == 4 ? 2 : 3;
