@@ -48,7 +48,7 @@ struct TreeMerge {
 
 struct tg_tree_plan {
     tg_shape shape{};
-    int32_t G = 0, max_draft = 0, tiles = 1;
+    int32_t G = 0, max_draft = 0, tiles = 1, m = 128;  // wide kernel: tiles of m rows
     bool host_only = true;
     bool any_pages = false;  // some head reserves a page
     int device = 0;
@@ -103,10 +103,10 @@ struct alignas(16) BlockHdr {
 };
 static_assert(sizeof(BlockHdr) == 32, "BlockHdr layout");
 
-// Shared memory: a Q tile of 128 rows per tile, the K / V ring, block headers, barriers. Rows that the plan's
+// Shared memory: a Q tile of M rows per tile, the K / V ring, block headers, barriers. Rows that the plan's
 // drafts never use are zeros, so that they cost the products little power: the steps that the loads bound
 // run under the power cap, whose clock goes down with what the padding rows multiply.
-template <int D, int TILES>
+template <int D, int TILES, int M>
 struct TreeLayout {
     static constexpr int kHalves = D / 64;             // 128-byte column halves
     static constexpr int kEntry = kBlock * D * 2;      // K or V of a block
@@ -118,7 +118,7 @@ struct TreeLayout {
     static constexpr int kLimit = TILES == 1 ? (228 * 1024) / 2 - 1024 : 227 * 1024;
     static constexpr int kThreads = 32 * (5 * TILES + 1);
     static constexpr uint32_t kCols = 256u * TILES;    // tensor-memory columns
-    static constexpr int kQTile = kRows * D * 2;
+    static constexpr int kQTile = M * D * 2;
     static constexpr int kEntries = (kLimit - TILES * kQTile - kControl) / kEntry < kMaxEntries
                                         ? (kLimit - TILES * kQTile - kControl) / kEntry
                                         : kMaxEntries;
@@ -283,14 +283,15 @@ __device__ __forceinline__ void clean_v(uint32_t v, int32_t nv, bool draft, unsi
 constexpr float kTanhNear = 0.4f;
 constexpr double kTanh[4] = {0.999999901901, -0.333313624587, 0.132709767556, -0.0475536034831};
 
-// Capped scores in log2 units, in place: c tanh(s scale / c) log2 e.
+// Capped scores in log2 units, in place: c tanh(s scale / c) log2 e. Lanes that hold no row do not count
+// for the choice of the form.
 template <int N>
-__device__ __forceinline__ void cap_scores(uint32_t (&sr)[N], const TreeArgs &a) {
+__device__ __forceinline__ void cap_scores(uint32_t (&sr)[N], const TreeArgs &a, bool live = true) {
     using namespace ptx;
     float far = 0.f;
 #pragma unroll
     for (int c = 0; c < N; c += 2) far = max3(far, fabsf(__uint_as_float(sr[c])), fabsf(__uint_as_float(sr[c + 1])));
-    if (__all_sync(0xffffffffu, far * a.cap_x <= kTanhNear)) {
+    if (__all_sync(0xffffffffu, !live || far * a.cap_x <= kTanhNear)) {
         const f2 c0 = pair(a.cap_p[0], a.cap_p[0]), c1 = pair(a.cap_p[1], a.cap_p[1]), c2 = pair(a.cap_p[2], a.cap_p[2]),
                  c3 = pair(a.cap_p[3], a.cap_p[3]);
 #pragma unroll
@@ -330,7 +331,8 @@ __device__ __forceinline__ void cap_scores(uint32_t (&sr)[N], const TreeArgs &a)
 // Query rows are (token, head of the group) pairs, contiguous per token in q, so one 3-D tensor
 // map box loads them in order; rows past the draft are loaded or stale and never stored. Drafted
 // K and V are a last block of up to 64 tokens with the mask applied to its scores.
-// TILES = 1 (up to 128 rows): two CTAs per SM, so one's softmax and output overlap the other's
+// M = 64 (up to 64 rows) halves what the padding rows cost in power and shared memory: a warp then
+// has 16 rows, on its first 16 lanes. TILES = 1 (up to 128 rows): two CTAs per SM, so one's softmax and output overlap the other's
 // products. TILES = 2 (up to 256 rows): one CTA per SM whose tiles share the K and V ring; wider
 // drafts (G = 8) take several row blocks.
 // What masked places hold cannot leak: scores are selected, not added to; V rows past the valid
@@ -338,13 +340,14 @@ __device__ __forceinline__ void cap_scores(uint32_t (&sr)[N], const TreeArgs &a)
 // drafted V row is taken out of the product and added back only for the rows that attend to it.
 // ------------------------------------------------------------------------------------------
 
-template <int D, int TILES, bool CAP>
-__global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2 : 1)
+template <int D, int TILES, int M, bool CAP>
+__global__ void __launch_bounds__(TreeLayout<D, TILES, M>::kThreads, TILES == 1 ? 2 : 1)
     tree_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap tm_q,
                 const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                 const __grid_constant__ CUtensorMap tm_kd, const __grid_constant__ CUtensorMap tm_vd) {
-    using TL = TreeLayout<D, TILES>;
+    using TL = TreeLayout<D, TILES, M>;
     using namespace ptx;
+    constexpr int RW = M / 4;  // rows of a warp
     constexpr unsigned FULL = 0xffffffffu;
     constexpr int KS = D / 16;
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -360,11 +363,11 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(control + TL::kControl - 16);
     volatile int32_t *abort_flag = reinterpret_cast<volatile int32_t *>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr uint32_t q_half = kRows * 128u;  // bytes of one column half of a Q tile
+    constexpr uint32_t q_half = M * 128u;  // bytes of one column half of a Q tile
 
     // the Q rows that no draft of the plan fills
-    for (int c = threadIdx.x; c < (kRows - a.q_rows) * 8 * TL::kHalves; c += TL::kThreads) {
-        const int hf = c / ((kRows - a.q_rows) * 8), r = c - hf * ((kRows - a.q_rows) * 8);
+    for (int c = threadIdx.x; c < (M - a.q_rows) * 8 * TL::kHalves; c += TL::kThreads) {
+        const int hf = c / ((M - a.q_rows) * 8), r = c - hf * ((M - a.q_rows) * 8);
         *reinterpret_cast<uint4 *>(smem + hf * q_half + a.q_rows * 128 + r * 16) = make_uint4(0u, 0u, 0u, 0u);
     }
     ptx::fence_async_smem();
@@ -516,7 +519,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
 #pragma unroll
                                 for (int qh = 0; qh < TL::kHalves; ++qh)
                                     tma_3d(sbase + t * TL::kQTile + qh * q_half, &tm_q, qh * 64, h * a.G,
-                                           s.tok0 + ((s.it.row0 + t * kRows) >> a.g_shift), q_full);
+                                           s.tok0 + ((s.it.row0 + t * M) >> a.g_shift), q_full);
                         }
                     }
                     if (__shfl_sync(FULL, bad, 0)) {
@@ -562,7 +565,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
         const int t = warp - 4 * TILES;
         if (lane == 0) {
             constexpr uint32_t hi_q = sdesc_hi(1024), hi_kv = sdesc_hi(TL::kGroup);
-            constexpr uint32_t id_s = idesc_bf16(kBlock, kRows, 0), id_o = idesc_bf16(D, kRows, 1);
+            constexpr uint32_t id_s = idesc_bf16(kBlock, M, 0), id_o = idesc_bf16(D, M, 1);
             const uint32_t tm = tmem + 256 * t, t_o = tm + 128;
             const uint32_t k_lo = sdesc_lo(ring, 16), v_lo = sdesc_lo(ring, 1024), q_lo = sdesc_lo(sbase + t * TL::kQTile, 16);
             bool ok = *abort_flag == 0;
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
                 if (!ok) break;
                 const volatile BlockHdr *hd = hdrs + (blk % kHdr);
                 const int32_t info = hd->flags;
-                const bool on = (info >> 16) > t * kRows;
+                const bool on = (info >> 16) > t * M;
                 if (!(info & kStop)) {
                     if (info & kFirst) {
                         ok = mbar_wait(q_full, static_cast<uint32_t>(qn) & 1u, a.wait_ns, abort_flag);
@@ -649,8 +652,9 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
     } else {
         // ================================ softmax warps ================================
         const int t = warp >> 2, qd = warp & 3;
-        const int w0 = kRows * t + 32 * qd;        // the warp's first row of the item
+        const int w0 = M * t + RW * qd;            // the warp's first row of the item
         const int i = w0 + lane;
+        const bool live = RW == 32 || lane < RW;   // M = 64: a warp's 16 rows are its first 16 lanes
         const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
         const uint32_t t_s = tmem + lanes + 256 * t, t_o = t_s + 128;
         float m = -INFINITY, le = 0.f;
@@ -677,7 +681,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
             const int32_t info = vh->flags;
             if (info & kStop) break;
             const int32_t nv = (info >> 8) & 0xFF, nrow = info >> 16;
-            const bool valid = i < nrow;
+            const bool valid = live && i < nrow;
             if (w0 >= nrow) {  // no row of this warp
                 ok = my_turn(blk);
                 pass_turn();
@@ -707,7 +711,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
             tmem_wait_ld();
             float sl2 = CAP ? 1.f : a.scale_log2;
             if (CAP) {
-                cap_scores<64>(sr, a);
+                cap_scores<64>(sr, a, live);
             } else if (sl2 < 0.f) {  // the maximum below is of the products: turn them under a negative scale
 #pragma unroll
                 for (int c = 0; c < 64; ++c) sr[c] ^= 0x80000000u;
@@ -731,7 +735,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
             for (int c = 0; c < 64; c += 2)
                 mr[(c >> 1) & 3] = max3(mr[(c >> 1) & 3], __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
             const float mx = max3(fmaxf(mr[0], mr[1]), mr[2], mr[3]) * sl2;
-            const bool up = mx > m + 8.f;
+            const bool up = live && mx > m + 8.f;
             if (__any_sync(FULL, up)) {
                 const float mn = up ? mx : m;
                 const float c0 = !up ? 1.f : (m == -INFINITY ? 0.f : ex2(m - mn));
@@ -802,7 +806,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES>::kThreads, TILES == 1 ? 2
             };
             const bool any_bad = __any_sync(FULL, bad != 0ull);
 #pragma unroll 1
-            for (int r16 = 0; r16 < 32 && w0 + r16 < nrow; r16 += 16) {
+            for (int r16 = 0; r16 < RW && w0 + r16 < nrow; r16 += 16) {
                 const int32_t ra = w0 + r16 + (lane >> 2), rb = ra + 8;  // this thread's two rows
                 const float ia = __shfl_sync(FULL, inv, r16 + (lane >> 2)), ib = __shfl_sync(FULL, inv, r16 + (lane >> 2) + 8);
                 const bool va = ra < nrow, vb = rb < nrow;
@@ -1789,18 +1793,16 @@ void build_items(tg_tree_plan *p, const int32_t *cap, int32_t num_workers) {
     p->n_workers = static_cast<int32_t>(nw);
 }
 
-template <int D, int TILES, bool CAP>
+template <int D, int TILES, int M>
 int set_smem() {
-    TG_TRY(cudaFuncSetAttribute(tree_kernel<D, TILES, CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                TreeLayout<D, TILES>::kBytes));
+    TG_TRY(cudaFuncSetAttribute(tree_kernel<D, TILES, M, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeLayout<D, TILES, M>::kBytes));
+    TG_TRY(cudaFuncSetAttribute(tree_kernel<D, TILES, M, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, TreeLayout<D, TILES, M>::kBytes));
     return TG_OK;
 }
-template <int D, int TILES>
-int set_smem_both() {
-    const int rc = set_smem<D, TILES, false>();
-    return rc != TG_OK ? rc : set_smem<D, TILES, true>();
+template <int D>
+int set_smem_wide(const tg_tree_plan *p) {
+    return p->m == 64 ? set_smem<D, 1, 64>() : p->tiles == 1 ? set_smem<D, 1, 128>() : set_smem<D, 2, 128>();
 }
-
 template <int NR>
 int set_smem_narrow_t() {
     TG_TRY(cudaFuncSetAttribute(tree_narrow_kernel<NR, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, NarrowLayout<NR>::kBytes));
@@ -1826,9 +1828,7 @@ struct DeviceScope {
 int tree_device_init(tg_tree_plan *p) {
     DeviceScope scope;
     TG_TRY(scope.enter(p->device));
-    const int rc = p->narrow         ? set_smem_narrow(p->narrow)
-                   : p->shape.D == 128 ? (p->tiles == 1 ? set_smem_both<128, 1>() : set_smem_both<128, 2>())
-                                     : (p->tiles == 1 ? set_smem_both<64, 1>() : set_smem_both<64, 2>());
+    const int rc = p->narrow ? set_smem_narrow(p->narrow) : p->shape.D == 128 ? set_smem_wide<128>(p) : set_smem_wide<64>(p);
     if (rc != TG_OK) return rc;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -1920,6 +1920,7 @@ int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft
     p->G = G;
     p->max_draft = max_draft;
     p->tiles = max_draft * G > kRows ? 2 : 1;
+    p->m = max_draft * G <= kRows / 2 ? kRows / 2 : kRows;
     p->rows_item = p->tiles == 2 ? 2 * kRows : max_draft * G;
     p->q_rows = p->tiles == 2 ? kRows : max_draft * G;
     // The narrow kernel, whose items cost more and whose tokens cost less, from the mean pages of a head
@@ -1932,9 +1933,9 @@ int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft
         p->narrow = rows <= 16 ? 16 : 32;
         p->smem_bytes = p->narrow == 16 ? NarrowLayout<16>::kBytes : NarrowLayout<32>::kBytes;
     } else if (s->D == 128) {
-        p->smem_bytes = p->tiles == 1 ? TreeLayout<128, 1>::kBytes : TreeLayout<128, 2>::kBytes;
+        p->smem_bytes = p->m == 64 ? TreeLayout<128, 1, 64>::kBytes : p->tiles == 1 ? TreeLayout<128, 1, 128>::kBytes : TreeLayout<128, 2, 128>::kBytes;
     } else {
-        p->smem_bytes = p->tiles == 1 ? TreeLayout<64, 1>::kBytes : TreeLayout<64, 2>::kBytes;
+        p->smem_bytes = p->m == 64 ? TreeLayout<64, 1, 64>::kBytes : p->tiles == 1 ? TreeLayout<64, 1, 128>::kBytes : TreeLayout<64, 2, 128>::kBytes;
     }
     p->host_only = host_only != 0;
     p->any_pages = pages > 0;
@@ -1983,18 +1984,18 @@ TreeFn narrow_fn(bool cap) {
     return cap ? tree_narrow_kernel<NR, true> : tree_narrow_kernel<NR, false>;
 }
 
+template <int D>
+TreeFn wide_fn(const tg_tree_plan *p, bool cap) {
+    if (p->m == 64) return cap ? tree_kernel<D, 1, 64, true> : tree_kernel<D, 1, 64, false>;
+    if (p->tiles == 1) return cap ? tree_kernel<D, 1, 128, true> : tree_kernel<D, 1, 128, false>;
+    return cap ? tree_kernel<D, 2, 128, true> : tree_kernel<D, 2, 128, false>;
+}
+
 int launch_tree_kernel(const tg_tree_plan *p, const TreeArgs &a, const CUtensorMap *tm, bool cap, cudaStream_t stream) {
     if (p->narrow)
-        return launch_tree(p, p->narrow == 16 ? narrow_fn<16>(cap) : narrow_fn<32>(cap),
-                           NarrowLayout<32>::kThreads, a, tm, stream);
-    if (p->shape.D == 128) {
-        if (p->tiles == 1)
-            return launch_tree(p, cap ? tree_kernel<128, 1, true> : tree_kernel<128, 1, false>, TreeLayout<128, 1>::kThreads, a, tm, stream);
-        return launch_tree(p, cap ? tree_kernel<128, 2, true> : tree_kernel<128, 2, false>, TreeLayout<128, 2>::kThreads, a, tm, stream);
-    }
-    if (p->tiles == 1)
-        return launch_tree(p, cap ? tree_kernel<64, 1, true> : tree_kernel<64, 1, false>, TreeLayout<64, 1>::kThreads, a, tm, stream);
-    return launch_tree(p, cap ? tree_kernel<64, 2, true> : tree_kernel<64, 2, false>, TreeLayout<64, 2>::kThreads, a, tm, stream);
+        return launch_tree(p, p->narrow == 16 ? narrow_fn<16>(cap) : narrow_fn<32>(cap), NarrowLayout<32>::kThreads, a, tm, stream);
+    const int threads = p->tiles == 1 ? TreeLayout<128, 1, 128>::kThreads : TreeLayout<128, 2, 128>::kThreads;
+    return launch_tree(p, p->shape.D == 128 ? wide_fn<128>(p, cap) : wide_fn<64>(p, cap), threads, a, tm, stream);
 }
 
 template <int D>
@@ -2034,7 +2035,7 @@ extern "C" void tg_tree_plan_destroy(tg_tree_plan *p) {
 extern "C" int tg_tree_plan_items(const tg_tree_plan *p, int32_t *n_items, int32_t *n_workers, int32_t *n_merge,
                                   int32_t *rows, int64_t *device_bytes, int32_t *items, int32_t *worker_off) {
     if (!p) return TG_EINVAL;
-    if (rows) *rows = p->narrow ? p->narrow : kRows * p->tiles;
+    if (rows) *rows = p->narrow ? p->narrow : p->m * p->tiles;
     if (n_items) *n_items = static_cast<int32_t>(p->items.size());
     if (n_workers) *n_workers = p->n_workers;
     if (n_merge) *n_merge = static_cast<int32_t>(p->merge.size());

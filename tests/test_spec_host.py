@@ -171,8 +171,9 @@ def _plan(cap, Hq, Hkv, T, D=128, workers=0, pages=1 << 20, **kw):
 
 
 @pytest.mark.parametrize("Hq,T,tokens,D,rows", [(8, 4, 4000, 128, 16), (8, 5, 4000, 128, 32), (8, 8, 4000, 128, 32),
-                                                (8, 9, 4000, 128, 128), (8, 8, 1000, 128, 128), (8, 4, 1000, 128, 16),
-                                                (8, 4, 200, 128, 128), (8, 4, 4000, 64, 128), (8, 33, 4000, 128, 256)])
+                                                (8, 9, 4000, 128, 64), (8, 8, 1000, 128, 64), (8, 4, 1000, 128, 16),
+                                                (8, 4, 200, 128, 64), (8, 4, 4000, 64, 64), (8, 33, 4000, 128, 256),
+                                                (8, 17, 4000, 128, 128), (8, 16, 4000, 64, 64)])
 def test_plan_kernel_by_rows_and_lengths(Hq, T, tokens, D, rows):
     assert tg.tg_tree_plan_items(_plan([tokens] * 4, Hq, 2, T, D=D))["rows"] == rows
 
