@@ -723,8 +723,8 @@ int tg_tree_plan_create(const tg_shape *shape, const int32_t *kv_cap, int32_t ma
                         int32_t num_workers, int32_t host_only, int32_t device,
                         int32_t wait_limit_us, tg_tree_plan **out);
 void tg_tree_plan_destroy(tg_tree_plan *p);
-/* Inspection: counts; the query rows (token, query head) that the plan's kernel takes at a time (16
- * or 32: the kernel for few rows and long heads; 64, 128 or 256: the other); and for non-NULL arrays the
+/* Inspection: counts; the query rows (token, query head) that the plan's kernel takes at a time (16:
+ * the kernel for few rows; 64, 128 or 256: the other); and for non-NULL arrays the
  * work items (n_items x 8 int32: b*Hkv + h, page_begin, page_end, partial slot (-1 = writes the final
  * output), first query row, 1 if the item takes the drafted tokens, reserved tokens, 0) and each
  * worker's first item [n_workers + 1]; items from worker_off[n_workers] on are taken by ticket. */

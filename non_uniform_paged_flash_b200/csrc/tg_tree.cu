@@ -56,7 +56,7 @@ struct tg_tree_plan {
     int32_t n_workers = 0;
     int32_t rows_item = 0;   // query rows of an item at most
     int32_t q_rows = 0;      // query rows that an item's Q load brings, per tile
-    int32_t narrow = 0;      // rows of the narrow kernel (16 or 32), 0: wide kernel
+    bool narrow = false;     // run by the narrow kernel
     int32_t smem_bytes = 0;
     int32_t n_slots = 0;
     std::vector<tg::TreeItem> items;      // each worker's items, then the dynamic ones
@@ -87,9 +87,9 @@ constexpr float kLn2 = 0.69314718055994530942f;
 
 // Block header flags.
 constexpr int32_t kFirst = 1, kLast = 2, kDraft = 4, kStop = 8;
-// The narrow kernel's, whose kFirst and kLast are per stream: the item's own ends, and whether it takes
-// the drafted tokens.
-constexpr int32_t kOpen = 16, kClose = 32, kTakesDraft = 64;
+// The narrow kernel's, whose kFirst and kLast are per stream: the item's own ends, whether it takes the
+// drafted tokens, and whether its first block is the second stream's.
+constexpr int32_t kOpen = 16, kClose = 32, kTakesDraft = 64, kOdd = 128;
 
 // What the block's consumers need to know, written by the producer before the block's K arrives.
 struct alignas(16) BlockHdr {
@@ -867,11 +867,10 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES, M>::kThreads, TILES == 1 
 }
 
 // ------------------------------------------------------------------------------------------
-// Narrow tree kernel (D = 128, up to 32 query rows: short drafts, and the single-token step), one
-// persistent CTA per SM. With few rows the wide kernel's 128-row products are mostly padding, which
-// costs power (its memory-bound steps ran at 1.5 GHz under the 1000 W cap), and one softmax thread
-// per row leaves most lanes idle. Here the products are turned over, so that tokens and head
-// dimensions fill the 128 lanes and the rows are the N side (NR = 16 or 32):
+// Narrow tree kernel (D = 128, up to 16 query rows: the single-token step and the shortest drafts), one
+// persistent CTA per SM. With so few rows one softmax thread per row leaves most lanes idle and the
+// wide kernel's tiles are mostly padding. Here the products are turned over, so that tokens and head
+// dimensions fill the 128 lanes and the rows are the N side (NR = 16):
 //   S^T [128 tokens][NR] = K Q^T           (A = K, B = Q, both K-major in shared memory)
 //   O^T [128 dims][NR]  += V^T P^T         (A = V as stored, M-major; B = P^T, written to shared
 //                                           memory by the softmax threads, N-major)
@@ -892,9 +891,9 @@ constexpr int kNPages = 8;
 constexpr float kNarrowSlack = 20.f;   // sums of 2^30 tokens' 2^20 |v| stay in fp32 up to |v| = 2^77
 constexpr float kNoScore = -1e30f;     // base of a row that has seen no score
 
-template <int NR>
+constexpr int kNarrowRows = 16;        // query rows
 struct NarrowLayout {
-    static constexpr int D = 128;
+    static constexpr int D = 128, NR = kNarrowRows;
     static constexpr int kEntry = kNBlock * D * 2;
     static constexpr int kGroup = 2048;                   // 8 tokens: an atom per 64-column half
     static constexpr int kQBox = NR * D * 2;
@@ -920,15 +919,15 @@ __device__ __forceinline__ uint32_t float_key(float x) {
 }
 __device__ __forceinline__ float key_float(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
 
-template <int NR, bool CAP>
-__global__ void __launch_bounds__(NarrowLayout<NR>::kThreads, 1)
+template <bool CAP>
+__global__ void __launch_bounds__(NarrowLayout::kThreads, 1)
     tree_narrow_kernel(const __grid_constant__ TreeArgs a, const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ CUtensorMap tm_kd, const __grid_constant__ CUtensorMap tm_vd) {
-    using NL = NarrowLayout<NR>;
+    using NL = NarrowLayout;
     using namespace ptx;
     constexpr unsigned FULL = 0xffffffffu;
-    constexpr int D = 128, NE = NL::kEntries;
+    constexpr int D = 128, NR = kNarrowRows, NE = NL::kEntries;
     extern __shared__ __align__(1024) unsigned char smem[];
     const uint32_t sbase = smem_addr(smem);
     const uint32_t ring = sbase + NL::kRing, pbuf = sbase + NL::kQBoxes * NL::kQBox;
@@ -1081,7 +1080,8 @@ __global__ void __launch_bounds__(NarrowLayout<NR>::kThreads, 1)
                     BlockHdr *hd = hdrs + (blk % kHdr);
                     // first and last block of each of the two streams
                     hd->flags = (j < 2 ? kFirst : 0) | (j >= nblk - 2 ? kLast : 0) | (is_draft ? kDraft : 0) | (j == 0 ? kOpen : 0) |
-                                (last ? kClose : 0) | (s.it.draft ? kTakesDraft : 0) | (nv << 8) | (sh.nrow << 16);
+                                (last ? kClose : 0) | (s.it.draft ? kTakesDraft : 0) |
+                                ((blk - j) & 1 ? kOdd : 0) | (nv << 8) | (sh.nrow << 16);
                     hd->tok0 = s.tok0;
                     hd->h = sh.h;
                     hd->slot = s.it.slot;
@@ -1149,8 +1149,8 @@ __global__ void __launch_bounds__(NarrowLayout<NR>::kThreads, 1)
         // of block blk - 4, which its softmax had read before that block's product was issued.
         if (lane == 0) {
             constexpr uint32_t hi_q = sdesc_hi(1024), hi_kv = sdesc_hi(NL::kGroup);
-            // P^T: 8 tokens of NR rows are an atom of 8 * kPitch bytes, swizzled by its row width
-            constexpr uint32_t hi_p = ((8 * NL::kPitch) >> 4) | (1u << 14) | ((NR == 32 ? 4u : 6u) << 29);
+            // P^T: 8 tokens of 16 rows are an atom of 256 bytes under the 32-byte swizzle (mode 6)
+            constexpr uint32_t hi_p = ((8 * NL::kPitch) >> 4) | (1u << 14) | (6u << 29);
             constexpr uint32_t id_s = idesc_bf16(NR, kRows, 0), id_o = idesc_bf16(NR, kRows, 1) | (1u << 15);
             const uint32_t k_lo = sdesc_lo(ring, 16), v_lo = sdesc_lo(ring, 1024), q_lo = sdesc_lo(sbase, 16), p_lo = sdesc_lo(pbuf, 16);
             bool ok = *abort_flag == 0;
@@ -1239,8 +1239,7 @@ __global__ void __launch_bounds__(NarrowLayout<NR>::kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(32 * qd) << 16;
         const uint32_t t_o = tmem + lanes + 256;
         const uint32_t p_row = pbuf + st * NL::kP + i * NL::kPitch;
-        // 16-byte chunk of a P row under the row width's swizzle
-        const uint32_t p_xor = NR == 32 ? ((i >> 1) & 3) : ((i >> 2) & 1);
+        const uint32_t p_xor = (i >> 2) & 1;  // which 16-byte half of a P row goes first under the 32-byte swizzle
         float *m_row = base_m + st * NR;
         f2 le[NR / 2];
         bool ok = *abort_flag == 0;
@@ -1436,11 +1435,11 @@ __global__ void __launch_bounds__(NarrowLayout<NR>::kThreads, 1)
             if (wg_any(!ok || !mbar_wait(o_done + 8 * st, ph, a.wait_ns, abort_flag))) ok = false;
             fence_after();
             // row sums over the warp's tokens: halves of the rows change sides with the lanes, so that
-            // NR values need about NR shuffles, not 5 NR; lane l ends with rows of index bits from l
+            // NR values need NR shuffles, not 5 NR; lane l ends with the row of index bits from l
             float v[NR];
 #pragma unroll
             for (int r = 0; r < NR / 2; ++r) split(le[r], v[2 * r], v[2 * r + 1]);
-            constexpr int STEPS = NR >= 32 ? 5 : 4;
+            constexpr int STEPS = 4;  // of the 5 that halve 32 lanes: NR = 2^4
 #pragma unroll
             for (int z = 0; z < STEPS; ++z) {
                 const int half = NR >> (z + 1);
@@ -1451,7 +1450,7 @@ __global__ void __launch_bounds__(NarrowLayout<NR>::kThreads, 1)
                     v[r] = mine + __shfl_xor_sync(FULL, other, 1 << z);
                 }
             }
-            if (NR == 16) v[0] += __shfl_xor_sync(FULL, v[0], 16);
+            v[0] += __shfl_xor_sync(FULL, v[0], 16);
             // lane l holds row sum_z bit_z(l) NR / 2^(z + 1)
             int32_t r_at = 0;
 #pragma unroll
@@ -1465,16 +1464,20 @@ __global__ void __launch_bounds__(NarrowLayout<NR>::kThreads, 1)
             const int32_t r_lo = st * HR;
             if (i < HR) {
                 const int32_t r = r_lo + i;
-                const float *s0 = reinterpret_cast<const float *>(smem + NL::kQBoxes * NL::kQBox), *s1 = s0 + NL::kP / 4;
+                // the stream of the item's first block comes first, whichever it is: an item gives the same bits
+                // wherever in a CTA's run it falls
+                const int f0 = info & kOdd ? 1 : 0, f1 = f0 ^ 1;
+                const float *sums0 = reinterpret_cast<const float *>(smem + NL::kQBoxes * NL::kQBox);
+                const float *s0 = sums0 + f0 * (NL::kP / 4), *s1 = sums0 + f1 * (NL::kP / 4);
                 const float l0 = (s0[r] + s0[NR + r]) + (s0[2 * NR + r] + s0[3 * NR + r]);
                 const float l1 = (s1[r] + s1[NR + r]) + (s1[2 * NR + r] + s1[3 * NR + r]);
-                const float m0 = base_m[r], m1 = base_m[NR + r];
+                const float m0 = base_m[f0 * NR + r], m1 = base_m[f1 * NR + r];
                 const float M = m0 != m0 || m1 != m1 ? NAN : fmaxf(m0, m1);
                 const float e0 = ex2(m0 - M), e1 = ex2(m1 - M);
                 const float L = l0 * e0 + l1 * e1;
                 const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);
-                weight[r] = used[0] ? e0 * inv : 0.f;
-                weight[NR + r] = used[1] ? e1 * inv : 0.f;
+                weight[r] = used[f0] ? e0 * inv : 0.f;
+                weight[NR + r] = used[f1] ? e1 * inv : 0.f;
                 if (r < nrow) {
                     const float l = L == 0.f ? -INFINITY : (M + lg2(L)) * kLn2;
                     const int32_t q = row0 + r;
@@ -1484,15 +1487,16 @@ __global__ void __launch_bounds__(NarrowLayout<NR>::kThreads, 1)
             }
             wg_sync();
             const unsigned long long bad = (info & kTakesDraft) ? *item_bad : 0ull;
-            const bool u0 = used[0], u1 = used[1];
+            const uint32_t f0 = info & kOdd ? 1u : 0u;
+            const bool u0 = used[f0], u1 = used[f0 ^ 1u];
             // out^T = w0 O0^T + w1 O1^T; thread i holds dimension i, so a warp writes 32 consecutive elements
             // of a row at a time
             constexpr int C = HR < 16 ? HR : 16;
 #pragma unroll 1
             for (int r8 = 0; r8 < HR && r_lo + r8 < nrow; r8 += C) {
                 uint32_t oa[C], ob[C];
-                tmem_ld<C>(t_o + r_lo + r8, oa);
-                tmem_ld<C>(t_o + 64 + r_lo + r8, ob);
+                tmem_ld<C>(t_o + 64 * f0 + r_lo + r8, oa);
+                tmem_ld<C>(t_o + 64 * (f0 ^ 1u) + r_lo + r8, ob);
                 tmem_wait_ld();
                 float x[C];
 #pragma unroll
@@ -1707,7 +1711,7 @@ bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // narrow one's; and the shares of the cost laid out ahead of time. Swept on the GQA batch (wide, 677 MB:
 // 131 us at 14 pages and 98 %, 133.8 at 12 and 95 %, 137 at 12 and 92 %) and the serving layer (narrow,
 // 5.1 GB: 784 us at 20 to 30 pages and 90 %, 810 at 20 and 95 %, 1004 at 20 and 100 %).
-constexpr int kItemCost = 14, kItemCostNarrow = 24;
+constexpr int kItemCost = 18, kItemCostNarrow = 24;
 constexpr int kMinShare = 4;    // pages of a worker in a step too small to fill the machine
 constexpr int kStaticPermille = 980, kStaticPermilleNarrow = 900;
 
@@ -1803,13 +1807,11 @@ template <int D>
 int set_smem_wide(const tg_tree_plan *p) {
     return p->m == 64 ? set_smem<D, 1, 64>() : p->tiles == 1 ? set_smem<D, 1, 128>() : set_smem<D, 2, 128>();
 }
-template <int NR>
-int set_smem_narrow_t() {
-    TG_TRY(cudaFuncSetAttribute(tree_narrow_kernel<NR, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, NarrowLayout<NR>::kBytes));
-    TG_TRY(cudaFuncSetAttribute(tree_narrow_kernel<NR, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, NarrowLayout<NR>::kBytes));
+int set_smem_narrow() {
+    TG_TRY(cudaFuncSetAttribute(tree_narrow_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, NarrowLayout::kBytes));
+    TG_TRY(cudaFuncSetAttribute(tree_narrow_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, NarrowLayout::kBytes));
     return TG_OK;
 }
-int set_smem_narrow(int32_t nr) { return nr == 16 ? set_smem_narrow_t<16>() : set_smem_narrow_t<32>(); }
 
 // Selects the plan's device for a scope and puts the caller's back.
 struct DeviceScope {
@@ -1828,7 +1830,7 @@ struct DeviceScope {
 int tree_device_init(tg_tree_plan *p) {
     DeviceScope scope;
     TG_TRY(scope.enter(p->device));
-    const int rc = p->narrow ? set_smem_narrow(p->narrow) : p->shape.D == 128 ? set_smem_wide<128>(p) : set_smem_wide<64>(p);
+    const int rc = p->narrow ? set_smem_narrow() : p->shape.D == 128 ? set_smem_wide<128>(p) : set_smem_wide<64>(p);
     if (rc != TG_OK) return rc;
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
@@ -1924,14 +1926,15 @@ int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft
     p->rows_item = p->tiles == 2 ? 2 * kRows : max_draft * G;
     p->q_rows = p->tiles == 2 ? kRows : max_draft * G;
     // The narrow kernel, whose items cost more and whose tokens cost less, from the mean pages of a head
-    // on at which it measured faster (256 or 128 sequences of 32/8 heads, us narrow : wide, by mean pages).
-    // 4 to 16 rows:  8: 104 : 87   23: 124 : 131   45: 175 : 184   90: 144 : 146   180: 259 : 314
-    // 32 rows:       8: 125 : 97   23: 168 : 151   45: 232 : 208   90: 174 : 170   180: 286 : 308
-    // (64 rows of a variant with NR = 64: 180: 199 : 134, its softmax no longer hidden by the loads.)
+    // on at which it measured faster (128 or 256 sequences of 32/8 heads, 4 and 12 rows, 1 s loops, us
+    // narrow : wide by mean pages):  8: 98 : 84 and 99 : 87   23: 121 : 137 and 124 : 135
+    // 45: 171 : 183 and 174 : 183   90: 141 : 145 and 142 : 148   180: 261 : 266 and 268 : 270;
+    // one sequence, 16 rows, 30000 tokens at 30 to 90 %: 28 : 38. (A variant of 32 rows measured 298 : 281
+    // at 180 pages and 166 : 144 at 23, with 32 rows in use, and 889 : 864 on the serving layer with 20.)
     const int32_t rows = max_draft * G;
-    if (s->D == 128 && rows <= 32 && pages >= BH * (rows <= 16 ? 16 : 112)) {
-        p->narrow = rows <= 16 ? 16 : 32;
-        p->smem_bytes = p->narrow == 16 ? NarrowLayout<16>::kBytes : NarrowLayout<32>::kBytes;
+    if (s->D == 128 && rows <= kNarrowRows && pages >= BH * 16) {
+        p->narrow = true;
+        p->smem_bytes = NarrowLayout::kBytes;
     } else if (s->D == 128) {
         p->smem_bytes = p->m == 64 ? TreeLayout<128, 1, 64>::kBytes : p->tiles == 1 ? TreeLayout<128, 1, 128>::kBytes : TreeLayout<128, 2, 128>::kBytes;
     } else {
@@ -1979,11 +1982,6 @@ int launch_tree(const tg_tree_plan *p, TreeFn fn, int threads, const TreeArgs &a
     return TG_OK;
 }
 
-template <int NR>
-TreeFn narrow_fn(bool cap) {
-    return cap ? tree_narrow_kernel<NR, true> : tree_narrow_kernel<NR, false>;
-}
-
 template <int D>
 TreeFn wide_fn(const tg_tree_plan *p, bool cap) {
     if (p->m == 64) return cap ? tree_kernel<D, 1, 64, true> : tree_kernel<D, 1, 64, false>;
@@ -1993,7 +1991,7 @@ TreeFn wide_fn(const tg_tree_plan *p, bool cap) {
 
 int launch_tree_kernel(const tg_tree_plan *p, const TreeArgs &a, const CUtensorMap *tm, bool cap, cudaStream_t stream) {
     if (p->narrow)
-        return launch_tree(p, p->narrow == 16 ? narrow_fn<16>(cap) : narrow_fn<32>(cap), NarrowLayout<32>::kThreads, a, tm, stream);
+        return launch_tree(p, cap ? tree_narrow_kernel<true> : tree_narrow_kernel<false>, NarrowLayout::kThreads, a, tm, stream);
     const int threads = p->tiles == 1 ? TreeLayout<128, 1, 128>::kThreads : TreeLayout<128, 2, 128>::kThreads;
     return launch_tree(p, p->shape.D == 128 ? wide_fn<128>(p, cap) : wide_fn<64>(p, cap), threads, a, tm, stream);
 }
@@ -2035,7 +2033,7 @@ extern "C" void tg_tree_plan_destroy(tg_tree_plan *p) {
 extern "C" int tg_tree_plan_items(const tg_tree_plan *p, int32_t *n_items, int32_t *n_workers, int32_t *n_merge,
                                   int32_t *rows, int64_t *device_bytes, int32_t *items, int32_t *worker_off) {
     if (!p) return TG_EINVAL;
-    if (rows) *rows = p->narrow ? p->narrow : p->m * p->tiles;
+    if (rows) *rows = p->narrow ? kNarrowRows : p->m * p->tiles;
     if (n_items) *n_items = static_cast<int32_t>(p->items.size());
     if (n_workers) *n_workers = p->n_workers;
     if (n_merge) *n_merge = static_cast<int32_t>(p->merge.size());

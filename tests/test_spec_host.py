@@ -170,7 +170,7 @@ def _plan(cap, Hq, Hkv, T, D=128, workers=0, pages=1 << 20, **kw):
                                   num_workers=workers, host_only=True, **kw)
 
 
-@pytest.mark.parametrize("Hq,T,tokens,D,rows", [(8, 4, 4000, 128, 16), (8, 5, 4000, 128, 32), (8, 8, 4000, 128, 32),
+@pytest.mark.parametrize("Hq,T,tokens,D,rows", [(8, 4, 4000, 128, 16), (8, 5, 4000, 128, 64), (8, 8, 4000, 128, 64),
                                                 (8, 9, 4000, 128, 64), (8, 8, 1000, 128, 64), (8, 4, 1000, 128, 16),
                                                 (8, 4, 200, 128, 64), (8, 4, 4000, 64, 64), (8, 33, 4000, 128, 256),
                                                 (8, 17, 4000, 128, 128), (8, 16, 4000, 64, 64)])
@@ -208,7 +208,7 @@ def test_plan_covers_every_page_once(seed):
     assert sorted(slots) == list(range(len(slots)))
 
 
-@pytest.mark.parametrize("T,workers", [(16, 296), (5, 148)])
+@pytest.mark.parametrize("T,workers", [(16, 296), (4, 148)])
 def test_plan_shares_are_even(T, workers):
     rng = np.random.default_rng(0)
     cap = rng.integers(500, 8000, size=512)
