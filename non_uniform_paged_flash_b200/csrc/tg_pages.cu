@@ -32,7 +32,9 @@ struct CopyArgs {
 };
 
 // One warp per (pair, K or V): a page's first `rows` rows are one contiguous run of bytes in the
-// pool, copied kCopyVec vectors a lane at a time (a whole bf16 page of D = 128 is one round).
+// pool, copied kCopyVec vectors a lane at a time (a whole bf16 page of D = 128 is one round). Bound:
+// DRAM: 554 MB of INT8 pages with their scales read and written in 94.5 us, 5.86 TB/s; few pages: the
+// load's and the store's latency (the tails of a fork 1.8 us, 2.6 us with one warp for K and V).
 __global__ void __launch_bounds__(kCopyWarps * 32) copy_pages_kernel(const __grid_constant__ CopyArgs a) {
     const int64_t w = static_cast<int64_t>(blockIdx.x) * kCopyWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
@@ -86,7 +88,8 @@ __device__ __forceinline__ int64_t kept_rows(const CompactArgs &a, int32_t bh) {
 // One warp per TPW entries of the keep list, whatever heads they belong to, so heads of very
 // different budgets cost the same per row. Lane l finds entry l's head (binary search of
 // keep_off, the same few cached words for every lane), its source and destination rows; then the
-// warp copies the K rows and the V rows 16 bytes a lane, the rows' addresses by shuffle.
+// warp copies the K rows and the V rows 16 bytes a lane, the rows' addresses by shuffle. Bound: DRAM
+// (figures at the launch); short lists: the search's dependent loads, then one round of copies.
 template <int TPW>
 __global__ void __launch_bounds__(kCompactWarps * 32) compact_kernel(const __grid_constant__ CompactArgs a) {
     constexpr unsigned FULL = 0xffffffffu;

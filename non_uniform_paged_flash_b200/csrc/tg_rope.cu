@@ -75,8 +75,9 @@ __device__ __forceinline__ uint4 repack(const ptx::f2 (&A)[2], const ptx::f2 (&B
 // angle to 2^-24 of a turn), their sines and cosines once in shared memory while the rows' loads
 // are in flight. Norm, weight and rotation stay in fp32, two elements an instruction; the only
 // rounding is the output's. Bound: DRAM (4 D bytes per head row): 32001 tokens of 32 + 8 heads of
-// D = 128 take 120 us, 5.46 TB/s. 8 CTAs per SM of 5 rows a lane measured best (3 rows of 256 threads
-// 145 us, 10 CTAs at fewer registers 128 us, 64 threads 122 us).
+// D = 128 take 120 us, 5.46 TB/s, and 134 us in 1 s loops, where the power limit takes the clock to
+// 1.75 GHz. 8 CTAs per SM of 5 rows a lane measured best (3 rows of 256 threads 145 us, 10 CTAs at fewer
+// registers 128 us, 64 threads 122 us, persistent CTAs that load the next token ahead 157 us).
 template <int LPH, bool INTER>
 __global__ void __launch_bounds__(kRopeThreads, 8) norm_rope_kernel(const __grid_constant__ RopeArgs a) {
     using ptx::f2;

@@ -335,6 +335,13 @@ __device__ __forceinline__ void cap_scores(uint32_t (&sr)[N], const TreeArgs &a,
 // has 16 rows, on its first 16 lanes. TILES = 1 (up to 128 rows): two CTAs per SM, so one's softmax and output overlap the other's
 // products. TILES = 2 (up to 256 rows): one CTA per SM whose tiles share the K and V ring; wider
 // drafts (G = 8) take several row blocks.
+// Bound: DRAM, at the clock that the power limit leaves (1.5 to 1.65 GHz of 1.97 with the step repeated).
+// 256 sequences of 32/8 heads, 4096 to 32768 tokens at 5 to 50 %, 5 drafted tokens: 5.13 GB in 856 us,
+// 5.99 TB/s. 64 sequences, 2048 to 8192 at 10 to 90 %, 16 drafted: 677 MB in 140 us, 4.8 TB/s (131 us at
+// the full clock), of which about 16 us are the first loads' latency, the shares' uneven ends and the
+// merge. 13 sequences, 8192 to 32768 at 30 to 90 %, 64 drafted, capped: 757 MB in 294 us, where the
+// softmax warps set the pace: per 64 tokens 2800 clocks of a warp's loads, polynomials and
+// exponentials, the tensor pipe 27 % and issue 38 % busy, at the power limit as well.
 // What masked places hold cannot leak: scores are selected, not added to; V rows past the valid
 // tokens are zeroed in shared memory before the product (0 * NaN); and an infinity or NaN in a
 // drafted V row is taken out of the product and added back only for the rows that attend to it.
@@ -662,7 +669,8 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES, M>::kThreads, TILES == 1 
         bool ok = *abort_flag == 0;
         // With two tiles and capped scores, the two warps of a scheduler take turns at the exponentials, so
         // that one's share of the special-function unit falls on the other's polynomials (64-token capped
-        // trees 293 -> 275 us; without a cap there is too little other work: 266 against 271 us).
+        // trees over 757 MB: 296 us against 315; without a cap there is too little other work: 271 us
+        // against 266).
         constexpr bool TURNS = TILES > 1 && CAP;
         auto my_turn = [&](int32_t blk) {
             return !TURNS || mbar_wait(turn + 8 * (4 * t + qd), static_cast<uint32_t>(t == 0 ? blk + 1 : blk) & 1u, a.wait_ns, abort_flag);
@@ -885,6 +893,8 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES, M>::kThreads, TILES == 1 
 // it by kNarrowSlack in log2 units (a score that stays below it is a true one, so the largest
 // probability is never under 1). Row sums stay in the threads, one per row, and are added across
 // threads once per item in a fixed order.
+// Bound: DRAM: one drafted token, 64 sequences of 32/8 heads, 2048 to 8192 tokens at 10 to 90 %: 661 MB
+// in 119 us with the merge, 5.56 TB/s; tensor pipe 4 % busy, issue 15 %.
 // ------------------------------------------------------------------------------------------
 constexpr int kNBlock = 128;           // tokens of a block
 constexpr int kNPages = 8;
@@ -1550,7 +1560,7 @@ __global__ void __launch_bounds__(NarrowLayout::kThreads, 1)
 // Merge of the split heads: a warp per query row, by log-sum-exp over its parts in order (page
 // ranges ascending; a part that holds nothing has lse -inf). Lane j weighs part j; the parts'
 // loads do not wait for one another. Bound: one round of loads from L2, where the parts were just
-// written.
+// written (15 500 rows of D = 128 with 16 MB of parts: 12 us alone on a cold cache).
 // ------------------------------------------------------------------------------------------
 struct TreeMergeArgs {
     const TreeMerge *merge;
@@ -1708,9 +1718,12 @@ int token_map(CUtensorMap *tm, const void *base, int32_t D, int32_t heads, int64
 bool al16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Pages' worth of an item's fixed work (draft block, Q, joining, output), the wide kernel's and the
-// narrow one's; and the shares of the cost laid out ahead of time. Swept on the GQA batch (wide, 677 MB:
-// 131 us at 14 pages and 98 %, 133.8 at 12 and 95 %, 137 at 12 and 92 %) and the serving layer (narrow,
-// 5.1 GB: 784 us at 20 to 30 pages and 90 %, 810 at 20 and 95 %, 1004 at 20 and 100 %).
+// narrow one's; and the shares of the cost laid out ahead of time. Swept in 1 s loops. Wide: 64 sequences
+// of 32/8 heads, 2048 to 8192 tokens at 10 to 90 %, 16 drafted | 256 of 300 to 900 tokens, 8 drafted | 128
+// of 16/8 heads of D = 64: 18 pages and 98 % take 140.0 | 144.5 | 165.5 us, 10 and 98 % 141.2 | 150.0 |
+// 168.5, 14 and 95 % 143.3 | 142.0 | 169.1, 14 and 100 % 141.5 | 149.4 | 166.7. Narrow, the first of them
+// with 1 drafted token: 116.3 us at 20 to 30 pages and 90 %, 118 at 95 %, 126 at 30 and 100 %, 161 at 12
+// and 100 %.
 constexpr int kItemCost = 18, kItemCostNarrow = 24;
 constexpr int kMinShare = 4;    // pages of a worker in a step too small to fill the machine
 constexpr int kStaticPermille = 980, kStaticPermilleNarrow = 900;
