@@ -1876,6 +1876,9 @@ int tree_device_init(tg_tree_plan *p) {
         return TG_ENOMEM;
     }
     TG_TRY(cudaMemcpy(p->dev_base, img.data(), img.size(), cudaMemcpyHostToDevice));
+    // the call returns once pageable memory is staged; a stream that does not wait for the default one
+    // must find the plan complete
+    TG_TRY(cudaStreamSynchronize(cudaStreamLegacy));
     unsigned char *d = static_cast<unsigned char *>(p->dev_base);
     p->dev_bytes = at;
     p->d_items = reinterpret_cast<TreeItem *>(d + o_items);
