@@ -716,7 +716,8 @@ int tg_tree_masks(int32_t B, const int32_t *draft_off, const int32_t *parent, ui
  * calls on one plan share it, so they must be ordered (one stream, or events between).
  * Serves page = 16, D 64 or 128, G 1, 2, 4 or 8, pools below 2^27 pages, up to 65536 workers
  * (TG_EUNSUPPORTED otherwise).
- * TG_EINVAL for other bad arguments; TG_ENOMEM; *out is NULL on error. */
+ * TG_EINVAL for other bad arguments, among them reserved tokens with num_pages = 0; TG_ENOMEM; *out is
+ * NULL on error. */
 typedef struct tg_tree_plan tg_tree_plan;
 int tg_tree_plan_create(const tg_shape *shape, const int32_t *kv_cap, int32_t max_draft,
                         const int32_t *group_of_head, const int64_t *group_off, int32_t n_groups,
@@ -752,8 +753,9 @@ int tg_tree_plan_status(tg_tree_plan *p, tg_stream stream);
  * scale and softcap must be finite, softcap >= 0 (TG_EINVAL); page_table may be NULL when no head
  * reserves a page. bf16 products, fp32 accumulation, P rounded to bf16; deterministic. One kernel, and a merge
  * kernel (programmatic dependent) when the plan splits heads. Sequences whose draft does not fit
- * the plan or n_tokens, and lengths above the reserved ones, are skipped (TG_EBADPAGE through
- * tg_tree_plan_status; their rows are unspecified), as are bad page ids and rows. */
+ * the plan or n_tokens, lengths above the reserved ones and rows outside their group's table are
+ * skipped; a page id outside the pool reads page 0 instead. All are reported (TG_EBADPAGE through
+ * tg_tree_plan_status), and the rows concerned are unspecified. */
 int tg_tree_decode(tg_tree_plan *plan, int64_t n_tokens, const int32_t *draft_off, const void *q,
                    int64_t q_stride, const void *k_draft, int64_t k_stride, const void *v_draft,
                    int64_t v_stride, const uint64_t *tree_mask, const void *k_pages,

@@ -1926,6 +1926,7 @@ int tree_plan_create(const tg_shape *s, const int32_t *kv_cap, int32_t max_draft
         if (kv_cap[i] > TG_MAX_HEAD_TOKENS) return TG_EUNSUPPORTED;
         pages += (kv_cap[i] + 15) / 16;
     }
+    if (pages > 0 && s->num_pages < 1) return TG_EINVAL;  // reserved tokens need a pool: a bad page id reads its page 0
     // costs times workers stay in 64 bits
     if (pages > (1ll << 40) || num_workers > 65536) return TG_EUNSUPPORTED;
     for (int32_t g = 0; g < n_groups; ++g)
@@ -2093,7 +2094,7 @@ extern "C" int tg_tree_decode(tg_tree_plan *p, int64_t n_tokens, const int32_t *
     int cur = 0;
     TG_TRY(cudaGetDevice(&cur));
     if (cur != p->device) return TG_EINVAL;
-    // a pool of no page is never read; its map still needs an address
+    // without a pool no head reserves a page, so none is read; the maps still need an address
     const void *kp = s.num_pages > 0 ? k_pages : q, *vp = s.num_pages > 0 ? v_pages : q;
     const int64_t pool = s.num_pages > 0 ? s.num_pages : 1;
     CUtensorMap tm[5];
