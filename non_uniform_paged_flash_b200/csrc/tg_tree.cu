@@ -891,7 +891,9 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES, M>::kThreads, TILES == 1 
 // 2^(s - m) to stay in range, since floating point keeps the relative precision: m starts as the
 // score of the stream's first token and moves, with sums and O rescaled, only when a score exceeds
 // it by kNarrowSlack in log2 units (a score that stays below it is a true one, so the largest
-// probability is never under 1). Row sums stay in the threads, one per row, and are added across
+// probability is never under 1). A row's base moves by that row's scores alone, so neither the next
+// sequence's queries in the rows past a short draft nor a drafted key that only other rows attend to
+// changes a row's bits. Row sums stay in the threads, one per row, and are added across
 // threads once per item in a fixed order.
 // Bound: DRAM: one drafted token, 64 sequences of 32/8 heads, 2048 to 8192 tokens at 10 to 90 %: 661 MB
 // in 119 us with the merge, 5.56 TB/s; tensor pipe 4 % busy, issue 15 %.
@@ -899,6 +901,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES, M>::kThreads, TILES == 1 
 constexpr int kNBlock = 128;           // tokens of a block
 constexpr int kNPages = 8;
 constexpr float kNarrowSlack = 20.f;   // sums of 2^30 tokens' 2^20 |v| stay in fp32 up to |v| = 2^77
+constexpr float kNarrowLook = 19.f;    // excess from which the maxima are looked for
 constexpr float kNoScore = -1e30f;     // base of a row that has seen no score
 
 constexpr int kNarrowRows = 16;        // query rows
@@ -1350,9 +1353,11 @@ __global__ void __launch_bounds__(NarrowLayout::kThreads, 1)
                     split(fma2(pair(__uint_as_float(sr[r + 2]), __uint_as_float(sr[r + 3])), k, pair(-mm.z, -mm.w)), t2, t3);
                     top = max3(max3(top, t0, t1), t2, t3);
                 }
-                if (wg_any(top > kNarrowSlack)) {
-                    // Far above the base: the base moves to the exact maximum, sums and O with it. Rare, so
-                    // small code: the scores are read again, 8 rows at a time.
+                if (wg_any(top > kNarrowLook)) {
+                    // Far above the base: the base of such a row moves to the exact maximum, sums and O with it.
+                    // Rows that are not far keep theirs; since a row is looked at well before it is far, no other
+                    // row's scores decide about it. Rare, so small code: the scores are read again, 8 rows at a
+                    // time.
                     uint32_t *key = reinterpret_cast<uint32_t *>(weight + st * NR);
                     if (i < NR) key[i] = float_key(m[i] == m[i] ? m[i] : kNoScore);
                     wg_sync();
@@ -1371,10 +1376,12 @@ __global__ void __launch_bounds__(NarrowLayout::kThreads, 1)
                         }
                     }
                     wg_sync();
-                    float factor = 0.f, moved = 0.f;
+                    float factor = 1.f, moved = 0.f;
                     if (i < NR) {
-                        moved = m[i] == m[i] ? key_float(key[i]) : m[i];
-                        factor = ex2(m[i] - moved);
+                        const float most = key_float(key[i]);
+                        const bool far = most - m[i] > kNarrowSlack;  // false for a base of NaN or infinity
+                        moved = far ? most : m[i];
+                        factor = far ? ex2(m[i] - moved) : 1.f;
                     }
                     wg_sync();
                     if (i < NR) {
