@@ -283,15 +283,21 @@ __device__ __forceinline__ void clean_v(uint32_t v, int32_t nv, bool draft, unsi
 constexpr float kTanhNear = 0.4f;
 constexpr double kTanh[4] = {0.999999901901, -0.333313624587, 0.132709767556, -0.0475536034831};
 
-// Capped scores in log2 units, in place: c tanh(s scale / c) log2 e. Lanes that hold no row do not count
-// for the choice of the form.
+// Capped scores in log2 units, in place: c tanh(s scale / c) log2 e. The two forms differ in their last
+// bits, so only what counts may choose: a warp takes the polynomial where every score of its block
+// counts (`whole`) and all of them are small; lanes that hold no row of the item (`counts`) have no say.
+// Blocks with scores that do not count (stale rows of a page or of the ring, masked drafted tokens)
+// take the general form, on the 16-column groups that hold any of the n tokens. Zeroing such scores to
+// let the others choose cost every block more registers (16 drafted, capped: 164 us with the choice
+// left to all scores, 168 so, 175 to 182 with zeroed ones). Returns the choice.
 template <int N>
-__device__ __forceinline__ void cap_scores(uint32_t (&sr)[N], const TreeArgs &a, bool live = true) {
+__device__ __forceinline__ bool cap_scores(uint32_t (&sr)[N], const TreeArgs &a, bool whole, bool counts, int32_t n) {
     using namespace ptx;
     float far = 0.f;
 #pragma unroll
     for (int c = 0; c < N; c += 2) far = max3(far, fabsf(__uint_as_float(sr[c])), fabsf(__uint_as_float(sr[c + 1])));
-    if (__all_sync(0xffffffffu, !live || far * a.cap_x <= kTanhNear)) {
+    const bool near = __all_sync(0xffffffffu, whole && (!counts || far * a.cap_x <= kTanhNear));
+    if (near) {
         const f2 c0 = pair(a.cap_p[0], a.cap_p[0]), c1 = pair(a.cap_p[1], a.cap_p[1]), c2 = pair(a.cap_p[2], a.cap_p[2]),
                  c3 = pair(a.cap_p[3], a.cap_p[3]);
 #pragma unroll
@@ -308,11 +314,16 @@ __device__ __forceinline__ void cap_scores(uint32_t (&sr)[N], const TreeArgs &a,
         // tanh(x) = 1 - 2 / (1 + e^2x): absolute error of a few 2^-24 c, limits +-c
         const float k2 = 2.f * kLog2e * a.cap_x_signed;
 #pragma unroll
-        for (int c = 0; c < N; ++c) {
-            const float e = ex2(__uint_as_float(sr[c]) * k2);
-            sr[c] = __float_as_uint(a.cap2 * fmaf(-2.f, rcp(1.f + e), 1.f));
-        }
+        for (int b = 0; b < N; b += 16)
+            if (b < n) {
+#pragma unroll
+                for (int c = b; c < b + 16 && c < N; ++c) {
+                    const float e = ex2(__uint_as_float(sr[c]) * k2);
+                    sr[c] = __float_as_uint(a.cap2 * fmaf(-2.f, rcp(1.f + e), 1.f));
+                }
+            }
     }
+    return near;
 }
 
 // ------------------------------------------------------------------------------------------
@@ -719,7 +730,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES, M>::kThreads, TILES == 1 
             tmem_wait_ld();
             float sl2 = CAP ? 1.f : a.scale_log2;
             if (CAP) {
-                cap_scores<64>(sr, a, live);
+                cap_scores<64>(sr, a, sees == ~0ull, valid, nv);
             } else if (sl2 < 0.f) {  // the maximum below is of the products: turn them under a negative scale
 #pragma unroll
                 for (int c = 0; c < 64; ++c) sr[c] ^= 0x80000000u;
@@ -1320,8 +1331,13 @@ __global__ void __launch_bounds__(NarrowLayout::kThreads, 1)
                 tmem_wait_ld();
                 float *m = m_row;
                 float sl2 = a.scale_log2;
+                bool near = false;
                 if (CAP) {
-                    cap_scores<NR>(sr, a);
+                    if (nrow < NR) {  // rows that are not the item's
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) sr[r] = r < nrow ? sr[r] : 0u;
+                    }
+                    near = cap_scores<NR>(sr, a, !masked, true, NR);
                     sl2 = 1.f;
                 }
                 if (masked) {  // scores times scale, -inf where they do not count
@@ -1366,7 +1382,7 @@ __global__ void __launch_bounds__(NarrowLayout::kThreads, 1)
                         uint32_t x[8];
                         tmem_ld<8>(t_s + r8, x);
                         tmem_wait_ld();
-                        if (CAP) cap_scores<8>(x, a);
+                        if (CAP) cap_scores<8>(x, a, near, false, 8);
                         const uint32_t on = sees >> r8;
 #pragma unroll
                         for (int r = 0; r < 8; ++r) {

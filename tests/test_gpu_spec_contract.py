@@ -1,9 +1,11 @@
 """What the header promises of the speculative step at its edges (one B200): results that depend on
 nothing but what they are a function of, bit for bit."""
+import numpy as np
 import pytest
 import torch
 
 import non_uniform_paged_flash_b200 as tg
+from tests import _spec as sp
 from tests.test_gpu_tree import Batch
 
 pytestmark = pytest.mark.gpu
@@ -46,3 +48,77 @@ def test_finite_masked_drafted_keys_leave_their_non_readers_alone(G, T, factor):
     a = bits(bt, others)
     bt.k[1] = (bt.k[1].float() * factor).clamp(-1e37, 1e37).bfloat16()
     assert same(a, bits(bt, others))
+
+
+# ---- tree attention under a cap: only the scores that count choose the arithmetic ----
+
+FORMS = [(4, 128, [3, 4, 1], True), (4, 128, [3, 4, 1], False), (4, 64, [3, 4, 1], False), (1, 128, [20, 9, 3], False),
+         (8, 128, [12, 9, 3], False), (8, 128, [30, 9, 3], False)]
+
+
+@pytest.mark.parametrize("G,D,nd,few", FORMS)
+def test_capped_scores_ignore_stale_rows(G, D, nd, few):
+    """Whatever the pages' rows past a head's tokens hold, small, far or NaN: the same bits."""
+    got = []
+    for stale in (1e-3, 1e4, float("nan")):
+        bt = Batch(33, G, D, 2, [1, 17, 63, 66, 0, 129], nd, stale=stale, cap_extra=40, few=few)
+        got.append(bits(bt, slice(None), softcap=30.0))
+        bt.check(softcap=30.0)
+    assert same(got[0], got[1]) and same(got[0], got[2])
+
+
+@pytest.mark.parametrize("G,D,nd,few", FORMS)
+def test_capped_scores_ignore_earlier_items(G, D, nd, few):
+    """One worker takes a long head and then short ones: what the long one left in shared memory does not
+    reach them."""
+    bt = Batch(34, G, D, 1, [700, 10, 3], nd, few=few, workers=1)
+    rest = slice(nd[0], sum(nd))
+    a = bits(bt, rest, softcap=30.0)
+    rows = torch.from_numpy(sp.head_rows(bt.ids, bt.off, 0, 700)).cuda()
+    for x in ("kp", "vp"):
+        bt.dev[x].view(-1, D)[rows] *= 1000
+    assert same(a, bits(bt, rest, softcap=30.0))
+
+
+@pytest.mark.parametrize("G,D,nd,few", FORMS)
+def test_capped_scores_ignore_other_sequences_queries(G, D, nd, few):
+    bt = Batch(35, G, D, 2, [100, 33, 260, 17, 0, 5], nd, few=few)
+    first = slice(0, nd[0])
+    a = bits(bt, first, softcap=30.0)
+    bt.q[nd[0]:] *= 100
+    assert same(a, bits(bt, first, softcap=30.0))
+
+
+@pytest.mark.parametrize("G,D,T,few", [(4, 128, 4, True), (1, 128, 9, True), (4, 128, 9, False), (4, 64, 9, False),
+                                       (8, 128, 33, False)])
+@pytest.mark.parametrize("value", [40.0, 1e30, float("inf"), float("nan")])
+def test_capped_scores_ignore_masked_drafted_keys(G, D, T, few, value):
+    masks = [1 << j for j in range(T)]
+    masks = [m | (2 if j in (3, T - 1) else 0) for j, m in enumerate(masks)]
+    others = [t for t in range(T) if not masks[t] >> 1 & 1]
+    bt = Batch(36, G, D, 1, [37], [T], masks=masks, few=few)
+    a = bits(bt, others, softcap=30.0)
+    bt.k[1] = value
+    assert same(a, bits(bt, others, softcap=30.0))
+
+
+@pytest.mark.parametrize("G,D,nd,few", FORMS)
+@pytest.mark.parametrize("cap", [15.0, 30.0])
+def test_capped_scores_near_and_far(G, D, nd, few, cap):
+    """Small and large scores side by side: rows of both kinds in a warp, tokens of both kinds in a row."""
+    bt = Batch(37, G, D, 2, [100, 33, 260, 64, 129, 5], nd, few=few)
+    bt.q[::2] *= 20
+    bt.dev["kp"][::3] *= 8
+    bt.run(softcap=cap)
+    bt.check(softcap=cap)
+
+
+@pytest.mark.parametrize("T,few", [(4, False), (16, False), (40, False), (4, True)])
+def test_capped_repeats_are_bit_equal(T, few):
+    """Dynamic items, scores on both sides of the forms' border."""
+    rng = np.random.default_rng(2)
+    bt = Batch(38, 4, 128, 2, rng.integers(0, 2000, size=40), [T, 2, 3, 1] * 5, workers=20, few=few)
+    bt.q[::3] *= 8
+    a = bits(bt, slice(None), softcap=15.0)
+    for _ in range(10):
+        assert same(a, bits(bt, slice(None), softcap=15.0))
