@@ -804,9 +804,10 @@ int tg_copy_pages(int64_t num_pages, int32_t row_bytes, int64_t n_copies, const 
  * (bf16 [src_num_pages][16][D]), src_len[i] tokens. The source pools may be the destination pools
  * when no written page is also read. head_kv_len[i] receives the count. shape: B, Hkv, D
  * (D % 8 == 0), page 16, num_pages of the destination. n_bad (device int32 [1], cleared by the
- * caller) grows by one per head whose list is unusable (offsets out of order or past n_keep, or
- * more than head_budget[i] tokens: nothing is written, length 0) and per row with a token or page
- * out of bounds (not written). One launch. */
+ * caller) grows by one per head whose list is unusable (its own offsets out of order, below 0 or past
+ * n_keep, or more than head_budget[i] tokens: nothing is written, length 0) and per row with a token
+ * or page out of bounds (not written, though counted in the length). Lists may share entries of
+ * keep_idx; heads whose offsets are out of order among the others are slower. One launch. */
 int tg_compact_kv(const tg_shape *shape, int64_t src_num_pages, const void *k_src,
                   const void *v_src, const int32_t *src_table, const int64_t *src_head_off,
                   const int32_t *src_len, const int64_t *keep_off, const int32_t *keep_idx,

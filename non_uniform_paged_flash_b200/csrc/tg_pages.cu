@@ -85,10 +85,61 @@ __device__ __forceinline__ int64_t kept_rows(const CompactArgs &a, int32_t bh) {
     return b < 0 || e < b || e > a.n_keep || e - b > max(0, a.budget[bh]) ? -1 : e - b;
 }
 
+// The head that entry i of keep is taken for: the last one whose list starts at or before i, by bisection
+// of keep_off (the same few cached words for every lane). With offsets out of order a list may have
+// entries that another head is found for, or share some with another list. [from, to) is the run of
+// entries around i that bisect the same way: a list that lies in the run of its first entry is found by
+// every entry of it, and any of its entries can tell. The others are copied by their head's warp.
+struct Owner {
+    int32_t head;
+    int64_t from, to;
+    __device__ __forceinline__ Owner(const CompactArgs &a, int64_t i) : head(0), from(LLONG_MIN), to(LLONG_MAX) {
+        for (int32_t hi = a.BH; hi - head > 1;) {
+            const int32_t mid = (head + hi) >> 1;
+            const int64_t at = a.keep_off[mid];
+            if (at <= i) {
+                head = mid;
+                from = max(from, at);
+            } else {
+                hi = mid;
+                to = min(to, at);
+            }
+        }
+    }
+    __device__ __forceinline__ bool owns(int64_t first, int64_t m) const { return from <= first && first + m <= to; }
+};
+
+// Pool rows of head bh's token `to` and of its source, entry i of keep; false when either is out of bounds.
+__device__ __forceinline__ bool kept_row(const CompactArgs &a, int32_t bh, int64_t i, int64_t to, int64_t &src, int64_t &dst) {
+    const int32_t from = a.keep[i];
+    int64_t sp = -1;
+    const int64_t dp = a.table[a.off[bh] + to / 16];
+    if (from >= 0 && from < a.src_len[bh]) sp = a.src_table[a.src_off[bh] + from / 16];
+    if (sp < 0 || sp >= a.src_pages || dp < 0 || dp >= a.num_pages) return false;
+    src = sp * 16 + from % 16;
+    dst = dp * 16 + to % 16;
+    return true;
+}
+
+// One warp: the whole list of head bh, a row at a time.
+__device__ __noinline__ void compact_apart(const CompactArgs &a, int32_t bh, int lane) {
+    const int64_t first = a.keep_off[bh], m = kept_rows(a, bh);
+    for (int64_t to = 0; to < m; ++to) {
+        int64_t src, dst;
+        if (!kept_row(a, bh, first + to, to, src, dst)) {
+            if (lane == 0) atomicAdd(a.n_bad, 1);
+            continue;
+        }
+        for (int c = lane; c < a.row_vec; c += 32) {
+            a.k_dst[dst * a.row_vec + c] = a.k_src[src * a.row_vec + c];
+            a.v_dst[dst * a.row_vec + c] = a.v_src[src * a.row_vec + c];
+        }
+    }
+}
+
 // One warp per TPW entries of the keep list, whatever heads they belong to, so heads of very
-// different budgets cost the same per row. Lane l finds entry l's head (binary search of
-// keep_off, the same few cached words for every lane), its source and destination rows; then the
-// warp copies the K rows and the V rows 16 bytes a lane, the rows' addresses by shuffle. Bound: DRAM
+// different budgets cost the same per row. Lane l finds entry l's head, its source and destination
+// rows; then the warp copies the K rows and the V rows 16 bytes a lane, the rows' addresses by shuffle. Bound: DRAM
 // (figures at the launch); short lists: the search's dependent loads, then one round of copies.
 template <int TPW>
 __global__ void __launch_bounds__(kCompactWarps * 32) compact_kernel(const __grid_constant__ CompactArgs a) {
@@ -96,35 +147,30 @@ __global__ void __launch_bounds__(kCompactWarps * 32) compact_kernel(const __gri
     const int lane = threadIdx.x & 31;
     const int64_t gtid = static_cast<int64_t>(blockIdx.x) * (kCompactWarps * 32) + threadIdx.x;
     ptx::grid_wait();
+    bool apart = false;  // this thread's head is not found by its entries
     if (gtid < a.BH) {
         const int64_t m = kept_rows(a, static_cast<int32_t>(gtid));
+        if (m > 0) {
+            const int64_t first = a.keep_off[gtid];
+            const Owner o(a, first);
+            apart = o.head != gtid || !o.owns(first, m);
+        }
         a.kv_len[gtid] = m < 0 ? 0 : static_cast<int32_t>(m);
         if (m < 0) atomicAdd(a.n_bad, 1);
     }
     const int64_t i = (gtid >> 5) * TPW + lane;  // keep-list entry of this lane
     int64_t src = -1, dst = -1;
     if (lane < TPW && i < a.n_keep) {
-        int32_t lo = 0, hi = a.BH;  // the last head whose list starts at or before i
-        while (hi - lo > 1) {
-            const int32_t mid = (lo + hi) >> 1;
-            if (a.keep_off[mid] <= i) lo = mid;
-            else hi = mid;
-        }
+        const Owner o(a, i);
+        const int32_t lo = o.head;
         const int64_t first = a.keep_off[lo];
         const int64_t m = kept_rows(a, lo);
-        if (first <= i && i - first < m) {
-            const int64_t to = i - first;
-            const int32_t from = a.keep[i];
-            int64_t sp = -1, dp = a.table[a.off[lo] + to / 16];
-            if (from >= 0 && from < a.src_len[lo]) sp = a.src_table[a.src_off[lo] + from / 16];
-            if (sp >= 0 && sp < a.src_pages && dp >= 0 && dp < a.num_pages) {
-                src = sp * 16 + from % 16;
-                dst = dp * 16 + to % 16;
-            } else {
-                atomicAdd(a.n_bad, 1);
-            }
+        if (first <= i && i - first < m && o.owns(first, m)) {
+            if (!kept_row(a, lo, i, i - first, src, dst)) atomicAdd(a.n_bad, 1);
         }
     }
+    for (uint32_t rest = __ballot_sync(FULL, apart); rest; rest &= rest - 1)
+        compact_apart(a, static_cast<int32_t>(gtid - lane) + __ffs(static_cast<int>(rest)) - 1, lane);
     if (!__any_sync(FULL, src >= 0)) return;
     // vector v of the warp's rows: row v / row_vec, K first, then V
     const int per = TPW * a.row_vec;

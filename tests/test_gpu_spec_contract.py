@@ -122,3 +122,44 @@ def test_capped_repeats_are_bit_equal(T, few):
     a = bits(bt, slice(None), softcap=15.0)
     for _ in range(10):
         assert same(a, bits(bt, slice(None), softcap=15.0))
+
+
+# ---- compaction: a head's length never counts rows that were not written ----
+
+@pytest.mark.parametrize("koff,budget", [([0, 10, 5, 15], [20] * 3), ([0, 4, 2, 50, 130], [40] * 4),
+                                         ([0, 10, 5, 7, 12, 40, 40, 60], [40] * 7), ([0, 10, 10, 15, 120], [20, 0, 5, 105]),
+                                         ([100, 120, 0, 20, 10, 30], [25] * 5), ([-3, 5, 9], [9, 9])]
+                         + [(None, seed) for seed in range(12)])
+@pytest.mark.parametrize("D", [64, 512])
+def test_compact_offsets_in_any_order(koff, budget, D):
+    """Each head's own offsets decide about its list, whatever the others are: in order, within the keep
+    list and within the budget, all of it is written and counted, though another list may name the same
+    entries; else none of it."""
+    rng = np.random.default_rng(0 if koff else budget)
+    if koff is None:
+        BH = int(rng.integers(1, 80))
+        koff = np.sort(rng.integers(0, 121, size=BH + 1))
+        for _ in range(int(rng.integers(0, 5))):
+            koff[rng.integers(0, BH + 1)] = rng.integers(-30, 180)
+        budget = rng.integers(0, 121, size=BH)
+    BH, koff, budget = len(koff) - 1, np.asarray(koff, np.int64), np.asarray(budget, np.int32)
+    n_keep = 120
+    keep = rng.integers(0, 200, size=n_keep).astype(np.int32)
+    sids, soff, spool = sp.tables(rng, np.full(BH, 13))
+    ids, off, pool = sp.tables(rng, -(-budget.astype(np.int64) // 16))
+    ks, vs = (sp.bf16(rng, spool, 16, D).cuda() for _ in range(2))
+    kd, vd = (sp.bf16(rng, pool, 16, D).cuda() for _ in range(2))
+    exp = [kd.cpu().view(-1, D).clone(), vd.cpu().view(-1, D).clone()]
+    n = torch.full((BH,), 9, dtype=torch.int32, device="cuda")
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = lambda a, t=None: torch.from_numpy(np.ascontiguousarray(a if t is None else a.astype(t))).cuda()
+    tg.tg_compact_kv(tg.make_shape(1, BH, BH, D, pool), ks, vs, cu(sids), cu(soff), cu(np.full(BH, 200), np.int32), cu(koff),
+                     cu(keep), kd, vd, cu(ids if ids.size else np.zeros(1, np.int32)), cu(off), cu(budget), n, bad)
+    m = np.diff(koff)
+    usable = (koff[:-1] >= 0) & (m >= 0) & (koff[1:] <= n_keep) & (m <= budget)
+    assert n.cpu().tolist() == np.where(usable, m, 0).tolist() and int(bad) == int((~usable).sum())
+    for i in np.flatnonzero(usable):
+        to, frm = sp.head_rows(ids, off, i, int(m[i])), sp.head_rows(sids, soff, i, 200)[keep[koff[i]:koff[i + 1]]]
+        for e, x in zip(exp, (ks, vs)):
+            e[to] = x.cpu().view(-1, D)[frm]
+    assert torch.equal(kd.cpu().view(-1, D), exp[0]) and torch.equal(vd.cpu().view(-1, D), exp[1])
