@@ -1765,13 +1765,18 @@ void build_items(tg_tree_plan *p, const int32_t *cap, int32_t num_workers) {
     for (int64_t i = 0; i < BH; ++i) order[static_cast<size_t>(i)] = static_cast<int32_t>(i);
     std::stable_sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return cap[x] > cap[y]; });
     // A step that leaves workers without kMinShare pages is bound by latency: items cost nothing extra
-    // there, every head goes to as many workers as it has shares, and nothing is left for tickets.
-    int64_t total = 0;
-    for (int64_t i = 0; i < BH; ++i) total += (cap[i] + 15) / 16;
+    // there, every head goes to as many workers as it has shares, and nothing is left for tickets. A head
+    // without pages, whose drafted tokens are all its work, counts as a page, so that such heads are
+    // dealt out and not left to one worker.
+    int64_t total = 0, empty = 0;
+    for (int64_t i = 0; i < BH; ++i) {
+        total += (cap[i] + 15) / 16;
+        empty += cap[i] == 0;
+    }
     total *= rblocks;
     const bool small = total < static_cast<int64_t>(num_workers) * kMinShare;
     const int32_t item_cost = small ? 0 : p->narrow ? kItemCostNarrow : kItemCost;
-    total += BH * rblocks * item_cost;
+    total += BH * rblocks * item_cost + (small ? empty * rblocks : 0);
     const int64_t nw = std::max<int64_t>(1, small ? std::min<int64_t>(num_workers, std::max<int64_t>(total / kMinShare, BH * rblocks)) : num_workers);
     const int64_t fixed = !small && nw > 1 && p->tiles == 1
                               ? total * (p->narrow ? kStaticPermilleNarrow : kStaticPermille) / 1000
@@ -1784,19 +1789,20 @@ void build_items(tg_tree_plan *p, const int32_t *cap, int32_t num_workers) {
     for (int32_t i : order)
         for (int32_t rb = 0; rb < rblocks; ++rb) {
             const int32_t pages = (cap[i] + 15) / 16;
+            const int32_t unit_cost = small && pages == 0 ? 1 : item_cost;  // beside its pages
             const int32_t first_slot = p->n_slots;
             const size_t first = p->items.size();
             int32_t at = 0;
             for (;;) {
                 int64_t room;  // pages this item may take
                 // the share is full when what is left of it would hold less than a block
-                while (w <= nw && done + (at == 0 ? item_cost : 0) + std::min(cut, pages - at) > fixed * w / nw) {
+                while (w <= nw && done + (at == 0 ? unit_cost : 0) + std::min(cut, pages - at) > fixed * w / nw) {
                     if (w == nw && fixed == total) break;  // all static: the last worker takes the rest
                     p->worker_off.push_back(static_cast<int32_t>(p->items.size()));
                     ++w;
                 }
                 if (w <= nw) {
-                    room = w == nw && fixed == total ? INT_MAX : fixed * w / nw - done - (at == 0 ? item_cost : 0);
+                    room = w == nw && fixed == total ? INT_MAX : fixed * w / nw - done - (at == 0 ? unit_cost : 0);
                 } else {
                     room = std::max<int64_t>(min_dyn, (total - done) / (2 * nw));
                     if (pages - at <= room + room / 2) room = pages - at;
@@ -1813,7 +1819,7 @@ void build_items(tg_tree_plan *p, const int32_t *cap, int32_t num_workers) {
                 it.cap = cap[i];
                 it.slot = -1;
                 p->items.push_back(it);
-                done += (end - at) + (at == 0 ? item_cost : 0);
+                done += (end - at) + (at == 0 ? unit_cost : 0);
                 at = end;
                 if (at == pages) break;
             }

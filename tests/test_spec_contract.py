@@ -21,3 +21,24 @@ def test_plan_needs_a_pool_for_reserved_tokens(cap, ok):
     with pytest.raises(tg.TGError) as e:
         _plan(cap, pages=0)
     assert e.value.status == tg.TG_EINVAL
+
+
+@pytest.mark.parametrize("T,G", [(16, 4), (4, 4), (64, 8)])
+@pytest.mark.parametrize("full,tokens", [(0, 0), (1, 600), (16, 64), (8, 1000), (60, 100), (300, 17), (256, 4000)])
+def test_plan_spreads_heads_without_tokens(T, G, full, tokens):
+    """A head that reserves nothing still has its drafted tokens: such heads are dealt out with the rest."""
+    BH = 512
+    cap = np.zeros(BH, np.int32)
+    cap[np.random.default_rng(0).permutation(BH)[:full]] = tokens
+    info = tg.tg_tree_plan_items(_plan(cap, T=T, Hq=8 * G, Hkv=8))
+    it, off = info["items"], info["worker_off"]
+    # an even share of the (head, row block) units, and as many more as a worker's share of the pages
+    # amounts to: a page is worth a unit at most in a step bound by latency, 1/18 of one in others
+    units, workers = BH * (2 if T * G > 256 else 1), info["n_workers"]
+    pages = units * full * -(-tokens // 16) / BH
+    per = np.diff(off)
+    assert per.max() <= units / workers + max(4, pages / (18 * workers)) + 2
+    if pages < 4 * workers:
+        assert off[-1] == len(it)                             # none by ticket
+        load = [int(np.maximum(it[a:b, 2] - it[a:b, 1], 1).sum()) for a, b in zip(off[:-1], off[1:])]
+        assert max(load) <= (pages + units) / workers + 12
