@@ -247,6 +247,8 @@ def _stream(stream):
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
     import torch
+    if not torch.cuda.is_initialized():  # brings CUDA up, or says why it cannot be
+        return torch.cuda.current_stream().cuda_stream
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 

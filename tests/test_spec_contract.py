@@ -42,3 +42,27 @@ def test_plan_spreads_heads_without_tokens(T, G, full, tokens):
         assert off[-1] == len(it)                             # none by ticket
         load = [int(np.maximum(it[a:b, 2] - it[a:b, 1], 1).sum()) for a, b in zip(off[:-1], off[1:])]
         assert max(load) <= (pages + units) / workers + 12
+
+
+def test_default_stream_before_cuda_is_up(monkeypatch):
+    """Without a stream argument a call asks torch for its current stream, which brings CUDA up or says why it
+    cannot be (no CUDA build, a forked child), with or without the entries that are faster once it is up."""
+    import torch
+
+    class Stream:
+        cuda_stream = 77
+
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    assert tg._stream(None) == 77
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    assert tg._stream(None) == 77
+    assert tg._stream(5) == 5 and tg._stream(Stream) == 77
+
+    def no_cuda():
+        raise AssertionError("Torch not compiled with CUDA enabled")
+
+    monkeypatch.setattr(torch.cuda, "current_stream", no_cuda)
+    with pytest.raises(AssertionError):
+        tg._stream(None)
