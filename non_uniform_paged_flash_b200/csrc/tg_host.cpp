@@ -359,14 +359,16 @@ extern "C" int tg_fork(tg_alloc *a, int32_t parent, int32_t child, int32_t n_hea
 
 extern "C" int tg_tree_masks(int32_t B, const int32_t *draft_off, const int32_t *parent, uint64_t *mask) {
     if (B < 0 || !draft_off || (B > 0 && draft_off[0] != 0)) return TG_EINVAL;
+    // all offsets before any parent: there are draft_off[B] of them where the offsets ascend
     for (int32_t b = 0; b < B; ++b) {
         const int64_t n = static_cast<int64_t>(draft_off[b + 1]) - draft_off[b];
         if (n < 0 || n > TG_MAX_DRAFT || (n > 0 && (!parent || !mask))) return TG_EINVAL;
-        for (int64_t j = 0; j < n; ++j) {
+    }
+    for (int32_t b = 0; b < B; ++b)
+        for (int32_t j = 0; j < draft_off[b + 1] - draft_off[b]; ++j) {
             const int32_t p = parent[draft_off[b] + j];
             if (p < -1 || p >= j) return TG_EINVAL;
         }
-    }
     for (int32_t b = 0; b < B; ++b)
         for (int32_t j = 0; j < draft_off[b + 1] - draft_off[b]; ++j) {
             const int32_t p = parent[draft_off[b] + j];

@@ -1,8 +1,14 @@
 """What the header promises of the speculative step's host side, at its edges (CPU)."""
+import os
+import shutil
+import subprocess
+
 import numpy as np
 import pytest
 
 import non_uniform_paged_flash_b200 as tg
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _plan(cap, T=4, Hq=8, Hkv=2, D=128, pages=1 << 20, workers=0):
@@ -66,3 +72,15 @@ def test_default_stream_before_cuda_is_up(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", no_cuda)
     with pytest.raises(AssertionError):
         tg._stream(None)
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_masks_refuse_offsets_out_of_order_unread(tmp_path):
+    exe, csrc = str(tmp_path / "mask_bounds"), os.path.join(ROOT, "non_uniform_paged_flash_b200", "csrc")
+    subprocess.check_call(["g++", "-std=c++17", "-O1", "-g", "-fsanitize=address,undefined", "-fno-sanitize-recover=all",
+                           "-I" + os.path.join(ROOT, "include"), "-I" + csrc,
+                           os.path.join(ROOT, "tests", "native", "mask_bounds.cpp"),
+                           os.path.join(csrc, "tg_host.cpp"), "-o", exe])
+    r = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert "refused" in r.stdout
