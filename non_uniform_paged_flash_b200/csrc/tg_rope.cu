@@ -248,6 +248,7 @@ extern "C" int tg_rope_frequencies(int32_t rot_dim, double base, int32_t scaling
         low = std::max(0.0, std::floor(pair_of(beta_fast)));
         high = std::min(rot_dim - 1.0, std::ceil(pair_of(beta_slow)));
         if (high <= low) high = low + 0.001;
+        if (pair_of(beta_slow) < 0.0) low = -1.0, high = -0.5;  // even the first pair turns less: all are slow
     }
     for (int32_t i = 0; i < half; ++i) {
         double f = std::pow(base, -2.0 * i / rot_dim);

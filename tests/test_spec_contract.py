@@ -1,4 +1,5 @@
 """What the header promises of the speculative step's host side, at its edges (CPU)."""
+import math
 import os
 import shutil
 import subprocess
@@ -72,6 +73,19 @@ def test_default_stream_before_cuda_is_up(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_stream", no_cuda)
     with pytest.raises(AssertionError):
         tg._stream(None)
+
+
+@pytest.mark.parametrize("orig,fast,slow", [(4096, 32.0, 1.0), (5, 32.0, 1.0), (1, 2.0, 0.5), (100, 50.0, 20.0),
+                                             (1 << 40, 32.0, 1.0), (64, 10.18, 10.0), (7, 1.2, 1.1)])
+@pytest.mark.parametrize("rot,base", [(64, 10000.0), (2, 10000.0), (128, 1.5), (10, 5e5)])
+def test_yarn_keeps_fast_pairs_and_interpolates_slow_ones(rot, base, orig, fast, slow):
+    """By the turns of each pair over the original length, also where every pair is slow or every one fast."""
+    plain = tg.tg_rope_frequencies(rot, base)[0]
+    yarn = tg.tg_rope_frequencies(rot, base, tg.TG_ROPE_YARN, 8.0, orig, fast, slow)[0]
+    turns = orig * plain / (2 * math.pi)
+    np.testing.assert_allclose(yarn[turns > fast], plain[turns > fast], rtol=1e-12)
+    np.testing.assert_allclose(yarn[turns < slow], plain[turns < slow] / 8, rtol=1e-12)
+    assert np.all(yarn <= plain * (1 + 1e-12)) and np.all(yarn >= plain / 8 * (1 - 1e-12))
 
 
 @pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
