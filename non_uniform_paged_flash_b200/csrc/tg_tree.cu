@@ -2151,7 +2151,8 @@ extern "C" int tg_tree_decode(tg_tree_plan *p, int64_t n_tokens, const int32_t *
     a.scale_log2 = scale * kLog2e;
     if (softcap > 0.f) {
         a.cap2 = softcap * kLog2e;
-        a.cap_x_signed = scale / softcap;
+        // finite, twice log2 e times it too, so that a score of zero stays one under the tiniest cap
+        a.cap_x_signed = std::min(std::max(scale / softcap, -1e38f), 1e38f);
         a.cap_x = std::fabs(a.cap_x_signed);
         double k = static_cast<double>(scale) / softcap;
         for (int i = 0; i < 4; ++i, k *= (static_cast<double>(scale) / softcap) * (static_cast<double>(scale) / softcap))

@@ -163,3 +163,15 @@ def test_compact_offsets_in_any_order(koff, budget, D):
         for e, x in zip(exp, (ks, vs)):
             e[to] = x.cpu().view(-1, D)[frm]
     assert torch.equal(kd.cpu().view(-1, D), exp[0]) and torch.equal(vd.cpu().view(-1, D), exp[1])
+
+
+# ---- caps at the ends of their range ----
+
+@pytest.mark.parametrize("softcap", [1e-45, 1e-40, 1e-37, 1e30])
+@pytest.mark.parametrize("D,few", [(64, False), (128, False), (128, True)])
+def test_caps_near_the_ends_of_fp32(softcap, D, few):
+    """A cap too small to divide by, and one too large to matter, with scores of zero among them."""
+    bt = Batch(39, 4, D, 2, [100, 33, 0, 17], [4, 3], few=few)
+    bt.q[::2] = 0
+    bt.run(softcap=softcap)
+    bt.check(softcap=softcap)
