@@ -50,56 +50,60 @@ def test_finite_masked_drafted_keys_leave_their_non_readers_alone(G, T, factor):
     assert same(a, bits(bt, others))
 
 
-# ---- tree attention under a cap: only the scores that count choose the arithmetic ----
+# ---- tree attention: only the scores that count choose the arithmetic, under a cap above all ----
 
 FORMS = [(4, 128, [3, 4, 1], True), (4, 128, [3, 4, 1], False), (4, 64, [3, 4, 1], False), (1, 128, [20, 9, 3], False),
          (8, 128, [12, 9, 3], False), (8, 128, [30, 9, 3], False)]
 
 
 @pytest.mark.parametrize("G,D,nd,few", FORMS)
-def test_capped_scores_ignore_stale_rows(G, D, nd, few):
+@pytest.mark.parametrize("cap", [30.0, 0.0])
+def test_scores_ignore_stale_rows(G, D, nd, few, cap):
     """Whatever the pages' rows past a head's tokens hold, small, far or NaN: the same bits."""
     got = []
     for stale in (1e-3, 1e4, float("nan")):
         bt = Batch(33, G, D, 2, [1, 17, 63, 66, 0, 129], nd, stale=stale, cap_extra=40, few=few)
-        got.append(bits(bt, slice(None), softcap=30.0))
-        bt.check(softcap=30.0)
+        got.append(bits(bt, slice(None), softcap=cap))
+        bt.check(softcap=cap)
     assert same(got[0], got[1]) and same(got[0], got[2])
 
 
 @pytest.mark.parametrize("G,D,nd,few", FORMS)
-def test_capped_scores_ignore_earlier_items(G, D, nd, few):
+@pytest.mark.parametrize("cap", [30.0, 0.0])
+def test_scores_ignore_earlier_items(G, D, nd, few, cap):
     """One worker takes a long head and then short ones: what the long one left in shared memory does not
     reach them."""
     bt = Batch(34, G, D, 1, [700, 10, 3], nd, few=few, workers=1)
     rest = slice(nd[0], sum(nd))
-    a = bits(bt, rest, softcap=30.0)
+    a = bits(bt, rest, softcap=cap)
     rows = torch.from_numpy(sp.head_rows(bt.ids, bt.off, 0, 700)).cuda()
     for x in ("kp", "vp"):
         bt.dev[x].view(-1, D)[rows] *= 1000
-    assert same(a, bits(bt, rest, softcap=30.0))
+    assert same(a, bits(bt, rest, softcap=cap))
 
 
 @pytest.mark.parametrize("G,D,nd,few", FORMS)
-def test_capped_scores_ignore_other_sequences_queries(G, D, nd, few):
+@pytest.mark.parametrize("cap", [30.0, 0.0])
+def test_scores_ignore_other_sequences_queries(G, D, nd, few, cap):
     bt = Batch(35, G, D, 2, [100, 33, 260, 17, 0, 5], nd, few=few)
     first = slice(0, nd[0])
-    a = bits(bt, first, softcap=30.0)
+    a = bits(bt, first, softcap=cap)
     bt.q[nd[0]:] *= 100
-    assert same(a, bits(bt, first, softcap=30.0))
+    assert same(a, bits(bt, first, softcap=cap))
 
 
 @pytest.mark.parametrize("G,D,T,few", [(4, 128, 4, True), (1, 128, 9, True), (4, 128, 9, False), (4, 64, 9, False),
                                        (8, 128, 33, False)])
 @pytest.mark.parametrize("value", [40.0, 1e30, float("inf"), float("nan")])
-def test_capped_scores_ignore_masked_drafted_keys(G, D, T, few, value):
+@pytest.mark.parametrize("cap", [30.0, 0.0])
+def test_scores_ignore_masked_drafted_keys(G, D, T, few, value, cap):
     masks = [1 << j for j in range(T)]
     masks = [m | (2 if j in (3, T - 1) else 0) for j, m in enumerate(masks)]
     others = [t for t in range(T) if not masks[t] >> 1 & 1]
     bt = Batch(36, G, D, 1, [37], [T], masks=masks, few=few)
-    a = bits(bt, others, softcap=30.0)
+    a = bits(bt, others, softcap=cap)
     bt.k[1] = value
-    assert same(a, bits(bt, others, softcap=30.0))
+    assert same(a, bits(bt, others, softcap=cap))
 
 
 @pytest.mark.parametrize("G,D,nd,few", FORMS)
