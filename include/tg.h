@@ -686,8 +686,8 @@ int tg_rope_frequencies(int32_t rot_dim, double base, int32_t scaling, double fa
  *   y = x * (mean_d x_d^2 + eps)^(-1/2) * w      (w = q_weight / k_weight, bf16 [D]; NULL: y = x)
  *   (a, b) -> rot_scale * (a cos t - b sin t, a sin t + b cos t), t = position[n] * inv_freq[i],
  * over the pairs i < rot_dim/2 of y's first rot_dim elements: (y[2i], y[2i+1]) with interleaved
- * != 0, else (y[i], y[i + rot_dim/2]); the rest of y is kept. fp32 throughout, t in fp64, one
- * rounding to bf16. q bf16 [n_tokens][Hq][D], k bf16 [n_tokens][Hkv][D] with token strides; Hq or
+ * != 0, else (y[i], y[i + rot_dim/2]); the rest of y is kept. fp32 throughout (the sum of x_d^2
+ * too, which ends at 3.4e38), t in fp64, one rounding to bf16. q bf16 [n_tokens][Hq][D], k bf16 [n_tokens][Hkv][D] with token strides; Hq or
  * Hkv may be 0 (that side is skipped, its pointers unused). position int32 [n_tokens], any value;
  * inv_freq device fp64 [rot_dim/2] (both may be NULL when rot_dim = 0). An output may be its own
  * input (same pointer and stride). TG_EUNSUPPORTED: D % 8 != 0, D > 256, or halves with
@@ -743,16 +743,18 @@ int tg_tree_plan_status(tg_tree_plan *p, tg_stream stream);
  * ignored; the token itself counts only if its bit is set):
  *   s = scale * q . k;  softcap > 0: s <- softcap * tanh(s / softcap);
  *   lse = ln sum exp(s), out = sum exp(s - lse) v;  nothing to attend to: out = 0, lse = -inf.
- * What other places hold (rows of a page past the head's tokens, drafted tokens outside the mask)
- * does not reach the result, infinities and NaN included.
+ * What other places hold (rows of a page past the head's tokens, drafted tokens outside the mask,
+ * other sequences) does not reach the result, not its last bit, infinities and NaN included.
  *   q bf16 [n_tokens][Hq][D], k_draft / v_draft bf16 [n_tokens][Hkv][D] (device, token strides);
  *   tree_mask device uint64 [n_tokens]; k_pages .. head_kv_len as tg_ragged_paged_decode;
  *   out bf16 [n_tokens][Hq][D] and lse fp32 [n_tokens][Hq], contiguous; rows behind the last
  *   sequence are left as they were. n_tokens: rows of these arrays, >= draft_off[B].
- * A drafted token alone (mask bit 0) is a decode step whose token is not in the cache yet.
+ * A drafted token alone (mask bit 0) is a decode step whose token is not in the cache yet; a token
+ * that needs no verification is read faster after its append, by tg_ragged_paged_decode.
  * scale and softcap must be finite, softcap >= 0 (TG_EINVAL); page_table may be NULL when no head
- * reserves a page. bf16 products, fp32 accumulation, P rounded to bf16; deterministic. One kernel, and a merge
- * kernel (programmatic dependent) when the plan splits heads. Sequences whose draft does not fit
+ * reserves a page. bf16 products, fp32 accumulation (P before its normalisation goes up to 2^20 on plans
+ * of 16 rows, 2^8 on others, so values beyond about 2^77 may overflow), P rounded to bf16;
+ * deterministic. One kernel, and a merge kernel (programmatic dependent) when the plan splits heads. Sequences whose draft does not fit
  * the plan or n_tokens, lengths above the reserved ones and rows outside their group's table are
  * skipped; a page id outside the pool reads page 0 instead. All are reported (TG_EBADPAGE through
  * tg_tree_plan_status), and the rows concerned are unspecified. */

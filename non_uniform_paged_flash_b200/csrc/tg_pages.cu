@@ -284,8 +284,8 @@ extern "C" int tg_compact_kv(const tg_shape *s, int64_t src_num_pages, const voi
     a.keep = keep_idx;
     a.kv_len = head_kv_len;
     a.n_bad = n_bad;
-    // 32 entries a warp (1.3 M kept rows of D = 128: 220 us, 6.1 TB/s, against 272 us with 8); lists too
-    // short to give every SM 16 such warps go 8 entries a warp (17 000 rows: 5.3 us against 9.5 us)
+    // 32 entries a warp (1.3 M kept rows of D = 128: 224 us, 6.0 TB/s, against 272 us with 8); lists too
+    // short to give every SM 16 such warps go 8 entries a warp (17 000 rows: 5.2 us against 9.5 us)
     const bool few = n_keep < 148 * 16 * 32;
     const int64_t threads = few ? (n_keep + 7) / 8 * 32 : n_keep;
     const int64_t most = threads > BH ? threads : BH;

@@ -347,12 +347,13 @@ __device__ __forceinline__ bool cap_scores(uint32_t (&sr)[N], const TreeArgs &a,
 // products. TILES = 2 (up to 256 rows): one CTA per SM whose tiles share the K and V ring; wider
 // drafts (G = 8) take several row blocks.
 // Bound: DRAM, at the clock that the power limit leaves (1.5 to 1.65 GHz of 1.97 with the step repeated).
-// 256 sequences of 32/8 heads, 4096 to 32768 tokens at 5 to 50 %, 5 drafted tokens: 5.13 GB in 856 us,
-// 5.99 TB/s. 64 sequences, 2048 to 8192 at 10 to 90 %, 16 drafted: 677 MB in 140 us, 4.8 TB/s (131 us at
+// 256 sequences of 32/8 heads, 4096 to 32768 tokens at 5 to 50 %, 5 drafted tokens: 5.13 GB in 854 us,
+// 6.01 TB/s. 64 sequences, 2048 to 8192 at 10 to 90 %, 16 drafted: 677 MB in 140 us, 4.8 TB/s (127 us at
 // the full clock), of which about 16 us are the first loads' latency, the shares' uneven ends and the
-// merge. 13 sequences, 8192 to 32768 at 30 to 90 %, 64 drafted, capped: 757 MB in 294 us, where the
-// softmax warps set the pace: per 64 tokens 2800 clocks of a warp's loads, polynomials and
-// exponentials, the tensor pipe 27 % and issue 38 % busy, at the power limit as well.
+// merge. 13 sequences, 8192 to 32768 at 30 to 90 %, 64 drafted, capped: 757 MB in 292 us (381 us where
+// scores pass 0.4 of the cap, so that the general form runs), set by the softmax warps' chain of loads,
+// polynomials and exponentials, 2800 clocks of a warp per 64 tokens: the tensor pipe is 32 % and issue
+// 37 % busy.
 // What masked places hold cannot leak: scores are selected, not added to; V rows past the valid
 // tokens are zeroed in shared memory before the product (0 * NaN); and an infinity or NaN in a
 // drafted V row is taken out of the product and added back only for the rows that attend to it.
@@ -907,7 +908,7 @@ __global__ void __launch_bounds__(TreeLayout<D, TILES, M>::kThreads, TILES == 1 
 // changes a row's bits. Row sums stay in the threads, one per row, and are added across
 // threads once per item in a fixed order.
 // Bound: DRAM: one drafted token, 64 sequences of 32/8 heads, 2048 to 8192 tokens at 10 to 90 %: 661 MB
-// in 119 us with the merge, 5.56 TB/s; tensor pipe 4 % busy, issue 15 %.
+// in 120 us with the merge, 5.55 TB/s; tensor pipe 4 % busy, issue 15 %.
 // ------------------------------------------------------------------------------------------
 constexpr int kNBlock = 128;           // tokens of a block
 constexpr int kNPages = 8;
