@@ -743,8 +743,9 @@ int tg_tree_plan_status(tg_tree_plan *p, tg_stream stream);
  * ignored; the token itself counts only if its bit is set):
  *   s = scale * q . k;  softcap > 0: s <- softcap * tanh(s / softcap);
  *   lse = ln sum exp(s), out = sum exp(s - lse) v;  nothing to attend to: out = 0, lse = -inf.
- * What other places hold (rows of a page past the head's tokens, drafted tokens outside the mask,
- * other sequences) does not reach the result, not its last bit, infinities and NaN included.
+ * What other rows of K and V hold (a page's past the head's tokens, drafted tokens' outside the mask),
+ * and what other sequences hold, does not reach the result, not its last bit, infinities and NaN
+ * included. (Under a cap the last bits may follow the queries of the sequence's other drafted tokens.)
  *   q bf16 [n_tokens][Hq][D], k_draft / v_draft bf16 [n_tokens][Hkv][D] (device, token strides);
  *   tree_mask device uint64 [n_tokens]; k_pages .. head_kv_len as tg_ragged_paged_decode;
  *   out bf16 [n_tokens][Hq][D] and lse fp32 [n_tokens][Hq], contiguous; rows behind the last
@@ -754,9 +755,9 @@ int tg_tree_plan_status(tg_tree_plan *p, tg_stream stream);
  * scale and softcap must be finite, softcap >= 0 (TG_EINVAL); page_table may be NULL when no head
  * reserves a page. bf16 products, fp32 accumulation (P before its normalisation goes up to 2^20 on plans
  * of 16 rows, 2^8 on others, so values beyond about 2^77 may overflow), P rounded to bf16;
- * deterministic. One kernel, and a merge kernel (programmatic dependent) when the plan splits heads. Sequences whose draft does not fit
- * the plan or n_tokens, lengths above the reserved ones and rows outside their group's table are
- * skipped; a page id outside the pool reads page 0 instead. All are reported (TG_EBADPAGE through
+ * deterministic. One kernel, and a merge kernel (programmatic dependent) when the plan splits heads.
+ * Sequences whose draft does not fit the plan or n_tokens, lengths above the reserved ones and rows
+ * outside their group's table are skipped; a page id outside the pool reads page 0 instead. All are reported (TG_EBADPAGE through
  * tg_tree_plan_status), and the rows concerned are unspecified. */
 int tg_tree_decode(tg_tree_plan *plan, int64_t n_tokens, const int32_t *draft_off, const void *q,
                    int64_t q_stride, const void *k_draft, int64_t k_stride, const void *v_draft,
